@@ -55,7 +55,9 @@ typedef enum {
   SSD_ERR_UNSUPPORTED = 2,    /* valid but outside what the kernels are built for */
   SSD_ERR_WORKSPACE = 3,      /* workspace NULL or smaller than the query returned */
   SSD_ERR_CUDA = 4,           /* a CUDA runtime call or launch failed */
-  SSD_ERR_DEVICE_TIMEOUT = 5  /* a kernel's bounded wait expired (see ssd_get_device_status) */
+  SSD_ERR_DEVICE_TIMEOUT = 5, /* a kernel's bounded wait expired (see ssd_get_device_status) */
+  SSD_ERR_INDEX = 6           /* a kernel met a slot or a sequence bound out of range, or a slot
+                                 named twice (see ssd_get_device_status) */
 } ssd_status;
 
 typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype;
@@ -363,9 +365,136 @@ ssd_status ssd_selective_scan_fwd(const void* x, const float* dt, const float* A
                                   ssd_dtype y_dtype, cudaStream_t stream);
 
 /*
+ * A Mamba block as a server runs it: packed prompts and single tokens, with caches.
+ *
+ * Rows are packed tokens, [ntok, width], with a row stride in elements of their own (a column
+ * range of a projection's output is such a tensor); the values of a row are contiguous.  A batch of
+ * nseq prompts is one packed tensor: sequence i has the rows cu_seqlens[i] .. cu_seqlens[i+1]-1,
+ * nseq + 1 int32 values in device memory that do not decrease and stay in [0, ntok].  A
+ * sequence may be empty.  Rows ahead of the first and behind the last sequence are not written.
+ *
+ * A cache holds what nslots sequences keep between calls.  slots[i] (int32, device memory; NULL:
+ * slot i) is the slot of sequence or row i.  A negative slot marks padding: its rows are not
+ * written and no slot changes.  A slot past the cache, or one that an earlier sequence of the
+ * same call names too, is left out in the same way and latched as SSD_ERR_INDEX, as are bounds
+ * that decrease or leave [0, ntok] (ssd_get_device_status reports it; the rows and slots of the
+ * other sequences are then as usual).  resume[i] (one byte, device memory; NULL: all zero) says
+ * whether prompt i continues from its slot (nonzero) or starts from zeros; either way the slot
+ * holds the state after the prompt when the call is done.  An empty prompt that resumes leaves
+ * its slot as it was.
+ *
+ * All of it is read by the kernels, so the calls can be captured and replayed with new bounds,
+ * slots and flags.  Outputs must not overlap inputs (taken over their whole extent, first row
+ * to last).  Row strides must be at least the row's width.  Alignment is that of the element;
+ * rows, strides and widths of 16-byte multiples take wide accesses.  Every pointer must belong to
+ * the current device.
+ *
+ * ssd_conv_silu_varlen: ssd_conv_silu over packed prompts with history:
+ *     out_t[c] = silu(bias[c] + sum_{k<kwidth} w[c,k] v_{t-kwidth+1+k}[c]),
+ *   v the sequence's rows of u, before them its slot's history (the last kwidth-1 inputs, or zeros).
+ *   u, out [ntok, cdim] in `io`; w [cdim, kwidth] float32, kwidth 1..8; bias [cdim] float32 or NULL;
+ *   conv_state [nslots, kwidth-1, cdim] in `io`, or NULL (every sequence fresh, nothing kept; then
+ *   slots and resume must be NULL).  kwidth 1 has no history: conv_state NULL.
+ */
+ssd_status ssd_conv_silu_varlen(const void* u, int64_t u_stride, const float* w,
+                                const float* bias, const int32_t* cu_seqlens, void* conv_state,
+                                const int32_t* slots, const uint8_t* resume, void* out,
+                                int64_t out_stride, int64_t ntok, int nseq, int64_t nslots,
+                                int cdim, int kwidth, ssd_dtype io, cudaStream_t stream);
+
+/* ssd_conv_silu_step: the same for one token of each of `batch` sequences: u, out [batch, cdim];
+ *   reads and moves on the history of each row's slot (conv_state as above; kwidth 2..8). */
+ssd_status ssd_conv_silu_step(void* conv_state, const void* u, int64_t u_stride, const float* w,
+                              const float* bias, const int32_t* slots, void* out,
+                              int64_t out_stride, int64_t batch, int64_t nslots, int cdim,
+                              int kwidth, ssd_dtype io, cudaStream_t stream);
+
+/*
+ * The selective scan (ssd_selective_scan_fwd) over packed prompts and for single tokens, with the
+ * step's bias and softplus and the SiLU output gate in the same kernel:
+ *     dt = softplus(dt_t[d] + dt_bias[d])      (softplus == 0: dt_t[d] + dt_bias[d])
+ *     h[n] <- exp(dt A[d,n]) h[n] + dt x_t[d] B_t[g,n]
+ *     y_t[d] = (sum_n C_t[g,n] h[n] + D[d] x_t[d]) * silu(z_t[d])      (z NULL: no gate)
+ *   x, z [rows, dim] in `io`; dt [rows, dim] in dt_dtype (SSD_F32 or `io`); B, C [rows, ngroups,
+ *   dstate] in `io`, the values of a row contiguous; y [rows, dim] in y_dtype (SSD_F32 or `io`);
+ *   A [dim, dstate], D, dt_bias [dim] float32 (D, dt_bias NULL = 0); state [nslots, dim, dstate]
+ *   float32.  Any dim, dstate 1..128; channel d reads group d / (dim / ngroups).  Float32
+ *   arithmetic, states kept in float32.
+ */
+typedef struct {
+  const void* x;
+  const void* dt;
+  const float* A;
+  const void* B;
+  const void* C;
+  const float* D;
+  const float* dt_bias;
+  const void* z;
+  void* y;
+  float* state;
+  const int32_t* slots;
+  int64_t x_stride, dt_stride, b_stride, c_stride, z_stride, y_stride;
+  int64_t nslots;
+  int32_t dim, dstate, ngroups;
+  int32_t io, dt_dtype, y_dtype; /* ssd_dtype */
+  int32_t softplus;
+} ssd_selective_args;
+
+/* ssd_selective_scan_varlen: packed prompts.  state NULL: every sequence starts from zeros and
+ *   nothing is kept (slots and resume must then be NULL).  max_seqlen: the length of the longest
+ *   sequence if the caller knows it (0: unknown, the mean length is taken); it only chooses the
+ *   plan, never the result's rows.  Where there are few channels and sequences for the GPU, sequences
+ *   are cut into chunks: one launch finds the state after each chunk, a second scans the chunks
+ *   from their entering states.  workspace: ssd_selective_varlen_workspace_size() bytes for the
+ *   same shape (0 is possible), 256-byte aligned, contents on entry ignored. */
+size_t ssd_selective_varlen_workspace_size(int64_t ntok, int nseq, int dim, int dstate,
+                                           int ngroups, int64_t max_seqlen);
+ssd_status ssd_selective_scan_varlen(const ssd_selective_args* args, const int32_t* cu_seqlens,
+                                     const uint8_t* resume, int64_t ntok, int nseq,
+                                     int64_t max_seqlen, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream);
+
+/* ssd_selective_step: one token of each of `batch` sequences, the state of each row's slot updated
+ *   in place. */
+ssd_status ssd_selective_step(const ssd_selective_args* args, int64_t batch,
+                              cudaStream_t stream);
+
+/*
+ * Group norm over the channels of each row with a SiLU gate (channels last): the cdim channels
+ * of a row form ngroups groups of neighbouring channels, and per row and group
+ *     v = y * silu(z)  (gate_first != 0)  or  y;   mu = mean(v) (center != 0) or 0
+ *     out = (v - mu) / sqrt(mean((v - mu)^2) + eps) * weight + bias   [* silu(z), gate_first == 0]
+ *   y [rows, cdim] in y_dtype, z [rows, cdim] in z_dtype or NULL (no gate), out [rows, cdim] in
+ *   out_dtype, each SSD_F32 or SSD_BF16 and each with its row stride; weight [cdim] float32, bias
+ *   [cdim] float32 or NULL; eps >= 0.  out may equal y where their types and strides are the same.
+ *   Float32 statistics.  Groups of up to 8192 channels, or up to 16384 where the group size and all
+ *   strides are multiples of 8 and all pointers 16-byte aligned (else SSD_ERR_UNSUPPORTED).
+ */
+ssd_status ssd_group_norm_gate(const void* y, int64_t y_stride, const float* weight,
+                               const float* bias, const void* z, int64_t z_stride, void* out,
+                               int64_t out_stride, int64_t rows, int cdim, int ngroups, float eps,
+                               int center, int gate_first, ssd_dtype y_dtype, ssd_dtype z_dtype,
+                               ssd_dtype out_dtype, cudaStream_t stream);
+
+/* ssd_group_norm_gate_bwd: its gradients for L = sum(dout * out).  y, weight, bias, z as given to the
+ *   forward (bias NULL: no dbias); dout [rows, cdim] in dout_dtype.  Outputs: dy [rows, cdim]
+ *   float32 and dz [rows, cdim] in z_dtype (NULL where z is), dense; dweight, dbias [cdim] float32.
+ *   The statistics are found again from y and z.  Sums over rows in a fixed order.  workspace:
+ *   ssd_group_norm_gate_bwd_workspace_size() bytes, 256-byte aligned. */
+size_t ssd_group_norm_gate_bwd_workspace_size(int64_t rows, int cdim, int ngroups);
+ssd_status ssd_group_norm_gate_bwd(const void* dout, int64_t dout_stride, const void* y,
+                                   int64_t y_stride, const float* weight, const float* bias,
+                                   const void* z, int64_t z_stride, float* dy, void* dz,
+                                   float* dweight, float* dbias, int64_t rows, int cdim,
+                                   int ngroups, float eps, int center, int gate_first,
+                                   ssd_dtype dout_dtype, ssd_dtype y_dtype, ssd_dtype z_dtype,
+                                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device status word that kernels latch
- * when a bounded wait expires (for the current device).  Returns SSD_OK,
- * SSD_ERR_DEVICE_TIMEOUT, or SSD_ERR_CUDA if the synchronisation itself failed.
+ * when a bounded wait expires or an index is out of range (for the current device; the first
+ * one latched is kept).  Returns SSD_OK, SSD_ERR_DEVICE_TIMEOUT, SSD_ERR_INDEX, or SSD_ERR_CUDA
+ * if the synchronisation itself failed.
  */
 ssd_status ssd_get_device_status(cudaStream_t stream);
 

@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libssd.so")
 SSD_F32, SSD_BF16 = 0, 1
 SSD_PATH_SIMT, SSD_PATH_TCGEN05 = 0, 1
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED",
-          3: "SSD_ERR_WORKSPACE", 4: "SSD_ERR_CUDA", 5: "SSD_ERR_DEVICE_TIMEOUT"}
+          3: "SSD_ERR_WORKSPACE", 4: "SSD_ERR_CUDA", 5: "SSD_ERR_DEVICE_TIMEOUT",
+          6: "SSD_ERR_INDEX"}
 
 # The symbols include/ssd.h declares (tests check that the library exports each one).
 EXPORTS = ("ssd_chunk_scan_workspace_size", "ssd_chunk_scan_path", "ssd_chunk_scan_fwd",
@@ -29,6 +30,9 @@ EXPORTS = ("ssd_chunk_scan_workspace_size", "ssd_chunk_scan_path", "ssd_chunk_sc
            "ssd_chunk_scan_bwd_workspace_size", "ssd_chunk_scan_bwd", "ssd_chunk_state_fwd",
            "ssd_state_pass",
            "ssd_conv_silu", "ssd_dt_softplus", "ssd_gate_silu", "ssd_selective_scan_fwd",
+           "ssd_conv_silu_varlen", "ssd_conv_silu_step", "ssd_selective_varlen_workspace_size",
+           "ssd_selective_scan_varlen", "ssd_selective_step", "ssd_group_norm_gate",
+           "ssd_group_norm_gate_bwd_workspace_size", "ssd_group_norm_gate_bwd",
            "ssd_status_string",
            "ssd_get_device_status", "ssd_version")
 
@@ -58,6 +62,16 @@ class ScanOptions(ctypes.Structure):
     """ssd_scan_options: the walk's plan and wait limit (tests and tuning; zeros = defaults)."""
     _fields_ = [("max_ctas", ctypes.c_int), ("plan", ctypes.c_int),
                 ("wait_limit_ns", ctypes.c_int64)]
+
+
+class SelectiveArgs(ctypes.Structure):
+    """ssd_selective_args: the tensors and sizes of the selective scan's served forms."""
+    _fields_ = ([(n, _vp) for n in ("x", "dt", "A", "B", "C", "D", "dt_bias", "z", "y", "state",
+                                    "slots")] +
+                [(n, _i64) for n in ("x_stride", "dt_stride", "b_stride", "c_stride", "z_stride",
+                                     "y_stride", "nslots")] +
+                [(n, ctypes.c_int32) for n in ("dim", "dstate", "ngroups", "io", "dt_dtype",
+                                               "y_dtype", "softplus")])
 
 
 def load():
@@ -106,6 +120,27 @@ def load():
                                                        _i32, _vp]
     lib.ssd_step.restype = _i32
     lib.ssd_step.argtypes = [_vp] * 8 + [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _vp]
+    lib.ssd_conv_silu_varlen.restype = _i32
+    lib.ssd_conv_silu_varlen.argtypes = [_vp, _i64] + [_vp] * 7 + [_i64, _i64, _i32, _i64, _i32,
+                                                                   _i32, _i32, _vp]
+    lib.ssd_conv_silu_step.restype = _i32
+    lib.ssd_conv_silu_step.argtypes = [_vp, _vp, _i64] + [_vp] * 4 + [_i64, _i64, _i64, _i32,
+                                                                      _i32, _i32, _vp]
+    lib.ssd_selective_varlen_workspace_size.restype = _sz
+    lib.ssd_selective_varlen_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32, _i64]
+    lib.ssd_selective_scan_varlen.restype = _i32
+    lib.ssd_selective_scan_varlen.argtypes = [_vp, _vp, _vp, _i64, _i32, _i64, _vp, _sz, _vp]
+    lib.ssd_selective_step.restype = _i32
+    lib.ssd_selective_step.argtypes = [_vp, _i64, _vp]
+    lib.ssd_group_norm_gate.restype = _i32
+    lib.ssd_group_norm_gate.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i32,
+                                        _i32, ctypes.c_float] + [_i32] * 5 + [_vp]
+    lib.ssd_group_norm_gate_bwd_workspace_size.restype = _sz
+    lib.ssd_group_norm_gate_bwd_workspace_size.argtypes = [_i64, _i32, _i32]
+    lib.ssd_group_norm_gate_bwd.restype = _i32
+    lib.ssd_group_norm_gate_bwd.argtypes = ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64] +
+                                            [_vp] * 4 + [_i64, _i32, _i32, ctypes.c_float] +
+                                            [_i32] * 5 + [_vp, _sz, _vp])
     lib.ssd_status_string.restype = ctypes.c_char_p
     lib.ssd_status_string.argtypes = [_i32]
     lib.ssd_get_device_status.restype = _i32
@@ -495,6 +530,285 @@ def step(state, x, dt, A, B, C, D, out=None, y_dtype=torch.float32):
                           _ptr(y), Bt, H, P, N, G, io, _code(y_dtype), _stream(dev))
     _check(rc, "ssd_step")
     return y
+
+
+# ---- packed prompts and single tokens with caches, and the group norm -------------------------
+
+
+def _row_stride(t, name, dtype, shape, device):
+    """Check a tensor of packed rows (any row stride, the values of a row contiguous) and give its
+    row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    stride, width = t.stride(), 1
+    for k in range(len(shape) - 1, 0, -1):
+        if shape[k] != 1 and stride[k] != width:
+            raise ValueError(f"the values of a row of {name} must be contiguous")
+        width *= shape[k]
+    if shape[0] <= 1:
+        return width
+    if stride[0] < width:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return stride[0]
+
+
+def _whole(t, name, dtype, shape, device):
+    """Check a contiguous tensor; a None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _first(t, name, ndim):
+    """The tensor whose device and shape the others follow."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
+    return t.device
+
+
+def _launch(fn, dev, *args):
+    """Call a C entry with `dev` current, on its current stream."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise SSDError(rc, fn.__name__)
+
+
+def _seqs(cu_seqlens, resume, dev):
+    """Pointers of a packed batch's bounds [nseq + 1] int32 and flags [nseq] (bool or uint8)."""
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or \
+            cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be a tensor of nseq + 1 bounds")
+    nseq = cu_seqlens.shape[0] - 1
+    cu = _whole(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+    if resume is None:
+        return nseq, cu, None
+    if not isinstance(resume, torch.Tensor) or resume.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("resume must be a bool or uint8 tensor")
+    return nseq, cu, _whole(resume, "resume", resume.dtype, (nseq,), dev)
+
+
+def _conv_cache(conv_state, dtype, Cd, K, dev):
+    if conv_state is None:
+        return None, 0
+    if not isinstance(conv_state, torch.Tensor) or conv_state.dim() != 3:
+        raise ValueError("conv_state must be a tensor [nslots, K-1, C]")
+    nslots = conv_state.shape[0]
+    p = _whole(conv_state, "conv_state", dtype, (nslots, K - 1, Cd), dev)
+    return (None, 0) if K == 1 else (p, nslots)
+
+
+def _kernel_width(w, Cd):
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a tensor [C, K]")
+    return w.shape[1]
+
+
+def conv_silu_varlen(u, w, cu_seqlens, bias=None, conv_state=None, slots=None, resume=None,
+                     out=None):
+    """Short causal depthwise convolution + SiLU over packed prompts, with the history a cache
+    keeps: u [T,C] (bf16 or f32, any row stride), w [C,K] f32, cu_seqlens [nseq+1] int32 on the
+    device, bias [C] f32 or None -> out [T,C] in u's dtype.
+
+    conv_state [nslots,K-1,C] in u's dtype holds each slot's last K-1 inputs and is updated in
+    place; slots [nseq] int32 (None: sequence i has slot i; negative: padding, left alone); resume
+    [nseq] bool says which sequences continue from their slot (None: none).  Rows outside the
+    sequences are not written.  Bad slots and bounds are left out and reported by
+    device_status()."""
+    dev = _first(u, "u", 2)
+    T, Cd = u.shape
+    K = _kernel_width(w, Cd)
+    io = _io(u)
+    us = _row_stride(u, "u", None, (T, Cd), dev)
+    nseq, cu, res = _seqs(cu_seqlens, resume, dev)
+    state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
+    if out is None:
+        out = torch.empty((T, Cd), dtype=u.dtype, device=dev)
+    os_ = _row_stride(out, "out", u.dtype, (T, Cd), dev)
+    _launch(load().ssd_conv_silu_varlen, dev, u.data_ptr(), us,
+            _whole(w, "w", torch.float32, (Cd, K), dev),
+            _whole(bias, "bias", torch.float32, (Cd,), dev), cu, state,
+            _whole(slots, "slots", torch.int32, (nseq,), dev), res, out.data_ptr(), os_, T, nseq,
+            nslots, Cd, K, io)
+    return out
+
+
+def conv_silu_step(conv_state, u, w, bias=None, slots=None, out=None):
+    """conv_silu_varlen for one token of each sequence: u [batch,C] -> out [batch,C]; conv_state
+    [nslots,K-1,C] is read and moved on in place (K 2..8)."""
+    dev = _first(u, "u", 2)
+    Bt, Cd = u.shape
+    K = _kernel_width(w, Cd)
+    io = _io(u)
+    us = _row_stride(u, "u", None, (Bt, Cd), dev)
+    state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
+    if out is None:
+        out = torch.empty((Bt, Cd), dtype=u.dtype, device=dev)
+    os_ = _row_stride(out, "out", u.dtype, (Bt, Cd), dev)
+    _launch(load().ssd_conv_silu_step, dev, state, u.data_ptr(), us,
+            _whole(w, "w", torch.float32, (Cd, K), dev),
+            _whole(bias, "bias", torch.float32, (Cd,), dev),
+            _whole(slots, "slots", torch.int32, (Bt,), dev), out.data_ptr(), os_, Bt, nslots, Cd,
+            K, io)
+    return out
+
+
+def _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, nseq, out, y_dtype):
+    dev = _first(x, "x", 2)
+    rows, dim = x.shape
+    io = _io(x)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a tensor [dim, dstate]")
+    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("B must be a tensor [rows, G, dstate]")
+    if not isinstance(dt, torch.Tensor):
+        raise TypeError("dt must be a torch.Tensor")
+    N, G = A.shape[1], B.shape[1]
+    if dt.dtype != torch.float32 and dt.dtype != x.dtype:
+        raise TypeError(f"dt must be float32 or {x.dtype}, got {dt.dtype}")
+    shape, bc = (rows, dim), (rows, G, N)
+    y_dtype = out.dtype if out is not None else y_dtype
+    y = torch.empty(shape, dtype=y_dtype, device=dev) if out is None else out
+    nslots = 0
+    if state is not None:
+        if not isinstance(state, torch.Tensor) or state.dim() != 3:
+            raise ValueError("state must be a tensor [nslots, dim, dstate]")
+        nslots = state.shape[0]
+    args = SelectiveArgs(
+        x.data_ptr(), dt.data_ptr(), _whole(A, "A", torch.float32, (dim, N), dev), B.data_ptr(),
+        C.data_ptr(), _whole(D, "D", torch.float32, (dim,), dev),
+        _whole(dt_bias, "dt_bias", torch.float32, (dim,), dev),
+        None if z is None else z.data_ptr(), y.data_ptr(),
+        _whole(state, "state", torch.float32, (nslots, dim, N), dev),
+        _whole(slots, "slots", torch.int32, (nseq,), dev),
+        _row_stride(x, "x", None, shape, dev), _row_stride(dt, "dt", None, shape, dev),
+        _row_stride(B, "B", x.dtype, bc, dev), _row_stride(C, "C", x.dtype, bc, dev),
+        0 if z is None else _row_stride(z, "z", x.dtype, shape, dev),
+        _row_stride(y, "out", y_dtype, shape, dev), nslots, dim, N, G, io, _code(dt.dtype),
+        _code(y_dtype), 1 if softplus else 0)
+    return dev, args, y
+
+
+def selective_varlen_workspace_size(ntok, nseq, dim, dstate, ngroups, max_seqlen=0):
+    return load().ssd_selective_varlen_workspace_size(ntok, nseq, dim, dstate, ngroups,
+                                                      max_seqlen)
+
+
+def selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None,
+                          softplus=False, state=None, slots=None, resume=None, out=None,
+                          y_dtype=torch.float32, max_seqlen=0, workspace=None):
+    """Selective scan over packed prompts: x, z [T,dim] (bf16 or f32), dt [T,dim] (f32 or x's
+    dtype), B, C [T,G,N] in x's dtype, each with any row stride; A [dim,N], D, dt_bias [dim] f32;
+    cu_seqlens [nseq+1] int32 on the device -> y [T,dim] in y_dtype (f32 or x's dtype).
+
+    dt + dt_bias goes through a softplus when `softplus` is set; z, where given, gates y with
+    silu(z).  state [nslots,dim,N] f32, slots and resume as conv_state, slots and resume of
+    conv_silu_varlen.  max_seqlen (0: unknown) only helps to choose the plan."""
+    nseq, cu, res = _seqs(cu_seqlens, resume, _first(x, "x", 2))
+    dev, args, y = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, nseq,
+                                   out, y_dtype)
+    lib = load()
+    T, ws, need = x.shape[0], None, 0
+    if nseq > 0:
+        need = lib.ssd_selective_varlen_workspace_size(T, nseq, args.dim, args.dstate,
+                                                       args.ngroups, max_seqlen)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, device=dev)
+        ws, need = workspace.data_ptr(), workspace.numel()
+    elif need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    _launch(lib.ssd_selective_scan_varlen, dev, ctypes.byref(args), cu, res, T, nseq, max_seqlen,
+            ws, need)
+    return y
+
+
+def selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
+                   slots=None, out=None, y_dtype=torch.float32):
+    """selective_scan_varlen for one token of each sequence: x, dt, z [batch,dim], B, C
+    [batch,G,N]; state [nslots,dim,N] f32 is updated in place at each row's slot."""
+    dev, args, y = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots,
+                                   x.shape[0], out, y_dtype)
+    _launch(load().ssd_selective_step, dev, ctypes.byref(args), x.shape[0])
+    return y
+
+
+def group_norm_gate(y, weight, bias=None, z=None, ngroups=1, eps=1e-5, center=False,
+                    gate_first=True, out=None, out_dtype=torch.float32):
+    """Group norm over each row's channels with a SiLU gate (channels last): y [rows,C], z [rows,C]
+    or None (f32 or bf16 each, any row stride), weight, bias [C] f32 -> out [rows,C].
+
+    v = y silu(z) (gate_first) or y; out = (v - mean) / sqrt(mean((v - mean)^2) + eps) weight +
+    bias per group of C / ngroups channels, times silu(z) when the gate comes last; the mean is
+    taken as 0 unless `center` is set (RMS norm)."""
+    dev = _first(y, "y", 2)
+    rows, Cd = y.shape
+    shape = (rows, Cd)
+    out_dtype = out.dtype if out is not None else out_dtype
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    _launch(load().ssd_group_norm_gate, dev, y.data_ptr(), _row_stride(y, "y", None, shape, dev),
+            _whole(weight, "weight", torch.float32, (Cd,), dev),
+            _whole(bias, "bias", torch.float32, (Cd,), dev),
+            None if z is None else z.data_ptr(),
+            0 if z is None else _row_stride(z, "z", None, shape, dev), out.data_ptr(),
+            _row_stride(out, "out", out_dtype, shape, dev), rows, Cd, ngroups, eps, bool(center),
+            bool(gate_first), _code(y.dtype), SSD_F32 if z is None else _code(z.dtype),
+            _code(out_dtype))
+    return out
+
+
+def group_norm_gate_bwd(dout, y, weight, bias=None, z=None, ngroups=1, eps=1e-5, center=False,
+                        gate_first=True, workspace=None):
+    """Gradients of L = sum(dout * out) through group_norm_gate.  Returns a dict: y [rows,C] f32,
+    z [rows,C] in z's dtype (or None), weight [C] f32, bias [C] f32 (or None)."""
+    lib = load()
+    dev = _first(y, "y", 2)
+    rows, Cd = y.shape
+    shape = (rows, Cd)
+    f32 = dict(dtype=torch.float32, device=dev)
+    strides = [_row_stride(t, n, None, shape, dev) for t, n in ((dout, "dout"), (y, "y"))]
+    zs = 0 if z is None else _row_stride(z, "z", None, shape, dev)
+    wp = _whole(weight, "weight", torch.float32, (Cd,), dev)
+    bp = _whole(bias, "bias", torch.float32, (Cd,), dev)
+    g = {"y": torch.empty(shape, **f32),
+         "z": None if z is None else torch.empty(shape, dtype=z.dtype, device=dev),
+         "weight": torch.empty((Cd,), **f32),
+         "bias": None if bias is None else torch.empty((Cd,), **f32)}
+    if workspace is None:
+        need = lib.ssd_group_norm_gate_bwd_workspace_size(rows, Cd, ngroups)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, device=dev)
+    _launch(lib.ssd_group_norm_gate_bwd, dev, dout.data_ptr(), strides[0], y.data_ptr(),
+            strides[1], wp, bp, _ptr(z), zs, g["y"].data_ptr(), _ptr(g["z"]),
+            g["weight"].data_ptr(), _ptr(g["bias"]), rows, Cd, ngroups, eps, bool(center),
+            bool(gate_first), _code(dout.dtype), _code(y.dtype),
+            SSD_F32 if z is None else _code(z.dtype), workspace.data_ptr(), workspace.numel())
+    return g
 
 
 def device_status(device=None):

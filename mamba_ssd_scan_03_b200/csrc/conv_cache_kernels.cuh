@@ -1,0 +1,243 @@
+// conv_cache_kernels.cuh -- the short causal depthwise convolution with SiLU of a Mamba block,
+// with the history a cache keeps between calls: over a packed batch of prompts of different
+// lengths, and for one token of each sequence.  "State Space Models (SSM)" (ultralytics.com
+// glossary), section "Da S4 a Mamba" (the short convolution ahead of the selective SSM) and
+// "Come funzionano gli SSM" (the recurrent form used during generation).
+//
+//   out_t[c] = silu(bias[c] + sum_{k<K} w[c,k] v_{t-K+1+k}[c])
+//
+// where v is the sequence's input u, preceded by its slot's history: the last K-1 inputs of what
+// the slot has seen (zeros for a fresh sequence).  The history leaves as the last K-1 rows of
+// (history, u), the inputs' own bits.
+#pragma once
+#include "glue_kernels.cuh"
+
+namespace ssd {
+namespace cache {
+
+// Sites of the latched status word (ssd_common.cuh) that these kernels use.
+constexpr unsigned kSiteSeq = 200, kSiteSlot = 201;
+
+// VW neighbouring channels of a row: one vector access, or element by element for VW = 1.
+template <typename T, int VW>
+__device__ __forceinline__ void load_ch(const T* p, float (&v)[VW]) {
+  if constexpr (VW == 1) v[0] = io_traits<T>::load(p, 0);
+  else glue::vec<T>::load(p, v);
+}
+template <typename T, int VW>
+__device__ __forceinline__ void store_ch(T* p, const float (&v)[VW]) {
+  if constexpr (VW == 1) io_traits<T>::store(p, 0, v[0]);
+  else glue::vec<T>::store(p, v);
+}
+
+// A warp's answer: the slot of sequence i, or -1 where the sequence is to be left alone: a
+// negative slot (padding), one past the cache, or one that an earlier sequence of the call
+// names too (the last two are latched as SSD_ERR_INDEX).  Call with the whole warp.
+__device__ __forceinline__ int64_t warp_slot(const int* __restrict__ slots, int64_t i,
+                                             int64_t nslots) {
+  if (!slots) return i;
+  const int lane = threadIdx.x & 31;
+  const int s = slots[i];
+  if (s < 0) return -1;
+  bool bad = s >= nslots;
+  for (int64_t j = lane; j < i; j += 32) bad |= slots[j] == s;
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) latch_status(SSD_ERR_INDEX, kSiteSlot);
+    return -1;
+  }
+  return s;
+}
+
+// cu_seqlens must not decrease and must stay inside [0, ntok]; a warp latches SSD_ERR_INDEX
+// where it does not.  The kernels clip every access themselves.
+__device__ __forceinline__ void warp_check_seqs(const int* __restrict__ cu, int nseq,
+                                                int64_t ntok) {
+  bool bad = false;
+  for (int i = threadIdx.x & 31; i <= nseq; i += 32)
+    bad |= cu[i] < 0 || cu[i] > ntok || (i > 0 && cu[i] < cu[i - 1]);
+  if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0)
+    latch_status(SSD_ERR_INDEX, kSiteSeq);
+}
+
+template <typename T>
+struct ConvArgs {
+  const T* u;
+  const float* w;
+  const float* bias;
+  const int* cu;
+  T* state;
+  const int* slots;
+  const unsigned char* resume;
+  T* out;
+  int64_t us, os, ntok, nslots;  // row strides of u and out in elements
+  int nseq, cdim;
+};
+
+// Prompts.  One warp per (run of kRun packed rows, 32 groups of VW channels), a thread walking
+// its channels down the rows as conv_silu_kernel does: weights and the window in registers,
+// STEP rows' loads in flight together.  Only where a run meets the start of a sequence does
+// the window restart.  A run that holds a sequence's first row owns the sequence's first K-1
+// rows even where they reach past the run (the rows that read the history), and moves the
+// history on itself after reading it: no other warp touches the slot, so the update in place
+// needs no second launch and no ordering between CTAs.
+constexpr int kRun = 64;
+
+template <typename T, int K, int VW, int STEP>
+__global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
+  constexpr int W = K - 1 + STEP;
+  const int lane = threadIdx.x;
+  const unsigned ncb = (a.cdim + 32 * VW - 1) / (32 * VW);  // CTAs per run, neighbours in time
+  const unsigned run = blockIdx.x / ncb, cb = blockIdx.x % ncb;
+  const int c0 = int(cb * 32 + lane) * VW;
+  const bool live = c0 < a.cdim;  // VW > 1 only where cdim is a multiple of VW
+  const int64_t r0 = int64_t(run) * kRun;
+  const int64_t r1 = r0 + kRun < a.ntok ? r0 + kRun : a.ntok;
+  const T* ub = a.u + c0;
+  T* ob = a.out + c0;
+
+  if (run == 0) {
+    if (cb == 0) warp_check_seqs(a.cu, a.nseq, a.ntok);
+    // sequences of length zero have no first row: a fresh one leaves a history of zeros
+    if (K > 1 && a.state) {
+      for (int i0 = 0; i0 < a.nseq; i0 += 32) {
+        const int i = i0 + lane;
+        const bool z = i < a.nseq && a.cu[i] == a.cu[i + 1] && !(a.resume && a.resume[i]);
+        unsigned m = __ballot_sync(0xffffffffu, z);
+        while (m) {
+          const int j = i0 + __ffs(m) - 1;
+          m &= m - 1;
+          const int64_t s = warp_slot(a.slots, j, a.nslots);
+          if (s < 0 || !live) continue;
+          const float zero[VW] = {};
+          for (int k = 0; k < K - 1; ++k)
+            store_ch<T, VW>(a.state + (s * (K - 1) + k) * a.cdim + c0, zero);
+        }
+      }
+    }
+  }
+
+  // the first sequence that ends after r0
+  int seq = 0;
+  {
+    int n = 0;
+    for (int i0 = 0; i0 < a.nseq; i0 += 32) {
+      const int i = i0 + lane;
+      n += __popc(__ballot_sync(0xffffffffu, i < a.nseq && a.cu[i + 1] <= r0));
+    }
+    seq = n;
+  }
+
+  float wr[VW][K], bv[VW];
+#pragma unroll
+  for (int j = 0; j < VW; ++j) {
+    bv[j] = live && a.bias ? a.bias[c0 + j] : 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) wr[j][k] = live ? a.w[int64_t(c0 + j) * K + k] : 0.f;
+  }
+
+  for (int64_t r = r0; seq < a.nseq; ++seq) {
+    const int64_t s = a.cu[seq], e0 = a.cu[seq + 1];
+    if (s >= r1) break;
+    const int64_t e = e0 < a.ntok ? e0 : a.ntok;
+    if (e <= s || e <= r0 || s < 0) continue;
+    const bool head = s >= r0;  // the sequence starts in this run
+    // rows of this piece: from the sequence's start, or from the run's start but not the rows
+    // that belong to the run of the start; and, at a start, at least the first K-1 rows
+    int64_t b = head ? s : (s + K - 1 > r0 ? s + K - 1 : r0);
+    int64_t end = e < r1 ? e : r1;
+    if (head && s + K - 1 > end) end = s + K - 1 < e ? s + K - 1 : e;
+    if (b < r) b = r;  // rows of one piece never come before another's
+    const int64_t slot = a.state || a.slots ? warp_slot(a.slots, seq, a.nslots) : 0;
+    if (slot < 0 || b >= end) continue;
+    r = end;
+
+    float win[W][VW];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+      for (int j = 0; j < VW; ++j) win[k][j] = 0.f;
+    if (live) {
+      if (head) {
+        if (K > 1 && a.state) {
+          T* st = a.state + slot * (K - 1) * a.cdim + c0;
+          if (a.resume && a.resume[seq]) {
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) load_ch<T, VW>(st + int64_t(k) * a.cdim, win[k]);
+          }
+          // the history after this sequence: row k is position len - (K-1) + k; below zero it
+          // is a later row of the old history, which the ascending order has not overwritten
+          const int64_t len = e - s;
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) {
+            const int64_t pos = len - (K - 1) + k;
+            float v[VW] = {};
+            if (pos >= 0) load_ch<T, VW>(ub + (s + pos) * a.us, v);
+            else if (a.resume && a.resume[seq])
+              load_ch<T, VW>(st + (K - 1 + pos) * a.cdim, v);
+            store_ch<T, VW>(st + int64_t(k) * a.cdim, v);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) load_ch<T, VW>(ub + (b - (K - 1) + k) * a.us, win[k]);
+      }
+      for (int64_t t = b; t < end; t += STEP) {
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) {
+          if (t + i < end) load_ch<T, VW>(ub + (t + i) * a.us, win[K - 1 + i]);
+          else {
+#pragma unroll
+            for (int j = 0; j < VW; ++j) win[K - 1 + i][j] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) {
+          if (t + i < end) {
+            float o[VW];
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+              float acc = bv[j];
+#pragma unroll
+              for (int k = 0; k < K; ++k) acc = fmaf(wr[j][k], win[i + k][j], acc);
+              o[j] = glue::silu_fast(acc);
+            }
+            store_ch<T, VW>(ob + (t + i) * a.os, o);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) win[k][j] = win[k + STEP][j];
+      }
+    }
+  }
+}
+
+// One token of each sequence: a thread per (row, VW channels) reads its K-1 history rows and the
+// new one, writes the output and the moved history.
+template <typename T, int K, int VW>
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs<T> a) {
+  const int c0 = int(blockIdx.y * blockDim.x + threadIdx.x) * VW;
+  const int64_t row = blockIdx.x;
+  const int64_t slot = warp_slot(a.slots, row, a.nslots);
+  if (slot < 0 || c0 >= a.cdim) return;
+  T* st = a.state + slot * (K - 1) * a.cdim + c0;
+  float win[K][VW];
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) load_ch<T, VW>(st + int64_t(k) * a.cdim, win[k]);
+  load_ch<T, VW>(a.u + row * a.us + c0, win[K - 1]);
+  float o[VW];
+#pragma unroll
+  for (int j = 0; j < VW; ++j) {
+    float acc = a.bias ? a.bias[c0 + j] : 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) acc = fmaf(a.w[int64_t(c0 + j) * K + k], win[k][j], acc);
+    o[j] = glue::silu_fast(acc);
+  }
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) store_ch<T, VW>(st + int64_t(k) * a.cdim, win[k + 1]);
+  store_ch<T, VW>(a.out + row * a.os + c0, o);
+}
+
+}  // namespace cache
+}  // namespace ssd

@@ -881,6 +881,7 @@ const char* ssd_status_string(ssd_status s) {
     case SSD_ERR_WORKSPACE: return "SSD_ERR_WORKSPACE: workspace missing or too small";
     case SSD_ERR_CUDA: return "SSD_ERR_CUDA: CUDA launch or runtime failure";
     case SSD_ERR_DEVICE_TIMEOUT: return "SSD_ERR_DEVICE_TIMEOUT: a kernel's bounded wait expired";
+    case SSD_ERR_INDEX: return "SSD_ERR_INDEX: a kernel met a slot or a sequence bound out of range";
   }
   return "unknown ssd_status";
 }
@@ -1188,3 +1189,6 @@ extern "C" ssd_status ssd_chunk_scan_fwd_noalloc(
   if (st != SSD_OK) return st;
   return run_tc_walk(s, a, plan, scratch);
 }
+
+// Packed prompts and single tokens with caches, and the group norm.
+#include "block_lib.cuh"
