@@ -540,12 +540,15 @@ def _row_stride(t, name, dtype, shape, device):
     row stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is not None and t.dtype != dtype:
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+        return width
     stride, width = t.stride(), 1
     for k in range(len(shape) - 1, 0, -1):
         if shape[k] != 1 and stride[k] != width:
@@ -559,14 +562,14 @@ def _row_stride(t, name, dtype, shape, device):
 
 
 def _whole(t, name, dtype, shape, device):
-    """Check a contiguous tensor; a None stays None."""
+    """Check a contiguous tensor and give its address; a None stays None."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -576,24 +579,27 @@ def _whole(t, name, dtype, shape, device):
 
 
 def _first(t, name, ndim):
-    """The tensor whose device and shape the others follow."""
+    """Check the tensor whose device and shape the others follow; gives its device's index."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
-    return t.device
+    return t.get_device()
+
+
+def _empty(shape, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
 def _launch(fn, dev, *args):
-    """Call a C entry with `dev` current, on its current stream."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, stream)
+    """Call a C entry with device `dev` current, on its current stream."""
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
     if rc != 0:
         raise SSDError(rc, fn.__name__)
 
@@ -647,7 +653,7 @@ def conv_silu_varlen(u, w, cu_seqlens, bias=None, conv_state=None, slots=None, r
     nseq, cu, res = _seqs(cu_seqlens, resume, dev)
     state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
     if out is None:
-        out = torch.empty((T, Cd), dtype=u.dtype, device=dev)
+        out = _empty((T, Cd), u.dtype, dev)
     os_ = _row_stride(out, "out", u.dtype, (T, Cd), dev)
     _launch(load().ssd_conv_silu_varlen, dev, u.data_ptr(), us,
             _whole(w, "w", torch.float32, (Cd, K), dev),
@@ -667,7 +673,7 @@ def conv_silu_step(conv_state, u, w, bias=None, slots=None, out=None):
     us = _row_stride(u, "u", None, (Bt, Cd), dev)
     state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
     if out is None:
-        out = torch.empty((Bt, Cd), dtype=u.dtype, device=dev)
+        out = _empty((Bt, Cd), u.dtype, dev)
     os_ = _row_stride(out, "out", u.dtype, (Bt, Cd), dev)
     _launch(load().ssd_conv_silu_step, dev, state, u.data_ptr(), us,
             _whole(w, "w", torch.float32, (Cd, K), dev),
@@ -692,7 +698,7 @@ def _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, nseq,
         raise TypeError(f"dt must be float32 or {x.dtype}, got {dt.dtype}")
     shape, bc = (rows, dim), (rows, G, N)
     y_dtype = out.dtype if out is not None else y_dtype
-    y = torch.empty(shape, dtype=y_dtype, device=dev) if out is None else out
+    y = _empty(shape, y_dtype, dev) if out is None else out
     nslots = 0
     if state is not None:
         if not isinstance(state, torch.Tensor) or state.dim() != 3:
@@ -737,10 +743,10 @@ def selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=No
         need = lib.ssd_selective_varlen_workspace_size(T, nseq, args.dim, args.dstate,
                                                        args.ngroups, max_seqlen)
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, device=dev)
+        _need(workspace, "workspace", torch.uint8, device=x.device)
         ws, need = workspace.data_ptr(), workspace.numel()
     elif need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty((need,), torch.uint8, dev)
         ws = workspace.data_ptr()
     _launch(lib.ssd_selective_scan_varlen, dev, ctypes.byref(args), cu, res, T, nseq, max_seqlen,
             ws, need)
@@ -770,7 +776,7 @@ def group_norm_gate(y, weight, bias=None, z=None, ngroups=1, eps=1e-5, center=Fa
     shape = (rows, Cd)
     out_dtype = out.dtype if out is not None else out_dtype
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = _empty(shape, out_dtype, dev)
     _launch(load().ssd_group_norm_gate, dev, y.data_ptr(), _row_stride(y, "y", None, shape, dev),
             _whole(weight, "weight", torch.float32, (Cd,), dev),
             _whole(bias, "bias", torch.float32, (Cd,), dev),
@@ -790,19 +796,18 @@ def group_norm_gate_bwd(dout, y, weight, bias=None, z=None, ngroups=1, eps=1e-5,
     dev = _first(y, "y", 2)
     rows, Cd = y.shape
     shape = (rows, Cd)
-    f32 = dict(dtype=torch.float32, device=dev)
     strides = [_row_stride(t, n, None, shape, dev) for t, n in ((dout, "dout"), (y, "y"))]
     zs = 0 if z is None else _row_stride(z, "z", None, shape, dev)
     wp = _whole(weight, "weight", torch.float32, (Cd,), dev)
     bp = _whole(bias, "bias", torch.float32, (Cd,), dev)
-    g = {"y": torch.empty(shape, **f32),
-         "z": None if z is None else torch.empty(shape, dtype=z.dtype, device=dev),
-         "weight": torch.empty((Cd,), **f32),
-         "bias": None if bias is None else torch.empty((Cd,), **f32)}
+    g = {"y": _empty(shape, torch.float32, dev),
+         "z": None if z is None else _empty(shape, z.dtype, dev),
+         "weight": _empty((Cd,), torch.float32, dev),
+         "bias": None if bias is None else _empty((Cd,), torch.float32, dev)}
     if workspace is None:
         need = lib.ssd_group_norm_gate_bwd_workspace_size(rows, Cd, ngroups)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, device=dev)
+        workspace = _empty((max(need, 1),), torch.uint8, dev)
+    _need(workspace, "workspace", torch.uint8, device=y.device)
     _launch(lib.ssd_group_norm_gate_bwd, dev, dout.data_ptr(), strides[0], y.data_ptr(),
             strides[1], wp, bp, _ptr(z), zs, g["y"].data_ptr(), _ptr(g["z"]),
             g["weight"].data_ptr(), _ptr(g["bias"]), rows, Cd, ngroups, eps, bool(center),

@@ -1,6 +1,8 @@
 // block_lib.cuh -- the C ABI of a Mamba block as a server runs it and of its norm (declared in
 // include/ssd.h): argument checks, plans and launches.  Part of ssd_lib.cu, included at its end.
 #pragma once
+#include <atomic>
+
 #include "conv_cache_kernels.cuh"
 #include "norm_kernels.cuh"
 #include "selective_cache_kernels.cuh"
@@ -57,34 +59,52 @@ bool rows16(const void* p, int64_t stride, size_t es) {
 // ---- convolution -----------------------------------------------------------------------------
 
 template <typename T, int K, int VW>
-void launch_conv(const ssd::cache::ConvArgs<T>& a, bool step, cudaStream_t stream) {
-  namespace cc = ssd::cache;
-  if (step) {
-    if constexpr (K > 1) {
-      const dim3 grid(unsigned(a.ntok), unsigned((a.cdim + 128 * VW - 1) / (128 * VW)));
-      cc::conv_step_kernel<T, K, VW><<<grid, 128, 0, stream>>>(a);
-    }
-    return;
-  }
-  const int64_t runs = std::max<int64_t>(1, (a.ntok + cc::kRun - 1) / cc::kRun);
+void launch_conv(const ssd::cache::ConvArgs<T>& a, cudaStream_t stream) {
+  const int64_t runs = std::max<int64_t>(1, (a.ntok + a.run - 1) / a.run);
   const int64_t ncb = (a.cdim + 32 * VW - 1) / (32 * VW);
-  cc::conv_varlen_kernel<T, K, VW, VW == 1 ? 16 : 4>
+  ssd::cache::conv_varlen_kernel<T, K, VW, VW == 1 ? 16 : 8>
       <<<unsigned(runs * ncb), 32, 0, stream>>>(a);
+}
+template <typename T, int K, int VW>
+void launch_conv_step(const ssd::cache::ConvArgs<T>& a, cudaStream_t stream) {
+  const unsigned ncb = unsigned((a.cdim + 128 * VW - 1) / (128 * VW));
+  // four rows per thread where that still leaves every SM a few CTAs
+  if (a.ntok / 4 * ncb >= 2 * int64_t(sm_count()))
+    ssd::cache::conv_step_kernel<T, K, VW, 4>
+        <<<dim3(unsigned((a.ntok + 3) / 4), ncb), 128, 0, stream>>>(a);
+  else
+    ssd::cache::conv_step_kernel<T, K, VW, 1><<<dim3(unsigned(a.ntok), ncb), 128, 0, stream>>>(a);
 }
 
 template <typename T>
 void launch_conv_k(const ssd::cache::ConvArgs<T>& a, int kwidth, bool wide, bool step,
                    cudaStream_t stream) {
-  constexpr int VW = ssd::glue::vec<T>::VW;
-#define SSD_K(KW)                                                  \
-  case KW:                                                         \
-    if (wide) launch_conv<T, KW, VW>(a, step, stream);             \
-    else launch_conv<T, KW, 1>(a, step, stream);                   \
+#define SSD_K(KW)                                                                \
+  case KW:                                                                       \
+    if (step) {                                                                  \
+      if constexpr (KW > 1) {                                                    \
+        if (wide) launch_conv_step<T, KW, 2>(a, stream);                         \
+        else launch_conv_step<T, KW, 1>(a, stream);                              \
+      }                                                                          \
+    } else if (wide) {                                                           \
+      launch_conv<T, KW, 4>(a, stream);                                          \
+    } else {                                                                     \
+      launch_conv<T, KW, 1>(a, stream);                                          \
+    }                                                                            \
     break;
   switch (kwidth) {
     SSD_K(1) SSD_K(2) SSD_K(3) SSD_K(4) SSD_K(5) SSD_K(6) SSD_K(7) SSD_K(8)
   }
 #undef SSD_K
+}
+
+// Packed rows of a warp: 128 where that still gives every SM 32 warps (the weights and the
+// window's K-1 rows are read once per run), fewer otherwise.
+int conv_run(int64_t ntok, int cdim, int vw) {
+  const int64_t ncb = (cdim + 32 * vw - 1) / (32 * vw);
+  int run = 128;
+  while (run > 16 && (ntok + run - 1) / run * ncb < 32 * int64_t(sm_count())) run /= 2;
+  return run;
 }
 
 // Both forms: step (cu == NULL) has one row per sequence.
@@ -111,18 +131,19 @@ ssd_status run_conv(const void* u, int64_t us, const float* w, const float* bias
   const Arg outs[] = {rows_arg(out, ntok, os, cdim, es),
                       flat_arg(state, nslots * (kwidth - 1) * cdim, es)};
   if (!args_ok(in, outs)) return SSD_ERR_INVALID_ARG;
-  const int64_t runs = step ? ntok : std::max<int64_t>(1, (ntok + ssd::cache::kRun - 1) /
-                                                              ssd::cache::kRun);
-  if (ntok > INT32_MAX || nseq >= INT32_MAX || (cdim + 31) / 32 > 65535 ||
-      runs > INT32_MAX / ((cdim + 31) / 32))
+  if (ntok > INT32_MAX || nseq >= INT32_MAX || (cdim + 31) / 32 > 65535)
     return SSD_ERR_UNSUPPORTED;
-  const bool wide = cdim % (16 / int(es)) == 0 && rows16(u, us, es) && rows16(out, os, es) &&
-                    aligned16(state);
+  // four channels at a time: 8 or 16 bytes
+  const bool wide = cdim % 4 == 0 && us % 4 == 0 && os % 4 == 0 && aligned16(u) &&
+                    aligned16(out) && aligned16(state) && aligned16(w);
+  const int run = conv_run(ntok, cdim, wide ? 4 : 1);
+  if ((ntok + run - 1) / run * ((cdim + 31) / 32) > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   auto go = [&](auto* t) {
     using T = std::remove_reference_t<decltype(*t)>;
     const ssd::cache::ConvArgs<T> a{static_cast<const T*>(u), w, bias, cu,
                                     static_cast<T*>(state), slots, resume,
-                                    static_cast<T*>(out), us, os, ntok, nslots, int(nseq), cdim};
+                                    static_cast<T*>(out), us, os, ntok, nslots, int(nseq), cdim,
+                                    run};
     launch_conv_k<T>(a, kwidth, wide, step, stream);
   };
   if (io == SSD_BF16) go(static_cast<__nv_bfloat16*>(nullptr));
@@ -152,7 +173,7 @@ SelPlan make_sel_plan(int64_t ntok, int nseq, int dim, int dstate, int ngroups, 
     return int64_t(ngroups) * ((dpg + ch - 1) / ch);
   };
   const int64_t sched = 4 * int64_t(sm_count());  // warp schedulers
-  if (p.lpc == 4 && nseq * blocks(2) >= 2 * sched) p.r = 2;
+  (void)0;
   const int64_t len = std::min(ntok, maxlen > 0 ? maxlen : (ntok + nseq - 1) / nseq);
   const int64_t warps = nseq * blocks(p.r);
   p.chunk = 0;
@@ -220,7 +241,7 @@ ssd::cache::SelArgs sel_args(const ssd_selective_args* a) {
   return k;
 }
 
-template <int LPC, int R>
+template <typename T, typename TD, int LPC, int R, bool VEC>
 ssd_status launch_sel(const ssd::cache::SelArgs& k, const SelPlan& p, cudaStream_t stream) {
   namespace cc = ssd::cache;
   const int dpg = k.dim / k.ngroups, ch = sel_channels(LPC, R);
@@ -228,12 +249,39 @@ ssd_status launch_sel(const ssd::cache::SelArgs& k, const SelPlan& p, cudaStream
   if (p.units * ncb > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   const unsigned grid = unsigned(p.units * ncb);
   if (k.chunk) {
-    cc::selective_varlen_kernel<LPC, R, true><<<grid, 32, 0, stream>>>(k);
+    cc::selective_varlen_kernel<T, TD, LPC, R, VEC, true><<<grid, 32, 0, stream>>>(k);
     const ssd_status st = launched();
     if (st != SSD_OK) return st;
   }
-  cc::selective_varlen_kernel<LPC, R, false><<<grid, 32, 0, stream>>>(k);
+  cc::selective_varlen_kernel<T, TD, LPC, R, VEC, false><<<grid, 32, 0, stream>>>(k);
   return launched();
+}
+// Wide loads take whole rows of 8 or 16 states and channel groups that start and end on a lane's
+// eight channels, all 16-byte aligned.
+bool sel_wide(const ssd::cache::SelArgs& k) {
+  const size_t es = k.io_bf16 ? 2 : 4, ed = k.dt_bf16 ? 2 : 4, ey = k.y_bf16 ? 2 : 4;
+  return (k.dstate == 8 || k.dstate == 16) && (k.dim / k.ngroups) % 8 == 0 &&
+         rows16(k.x, k.xs, es) && rows16(k.dt, k.dts, ed) && rows16(k.B, k.bs, es) &&
+         rows16(k.C, k.cs, es) && (!k.z || rows16(k.z, k.zs, es)) && rows16(k.y, k.ys, ey);
+}
+
+template <typename T, typename TD>
+ssd_status launch_sel_shape(const ssd::cache::SelArgs& k, const SelPlan& p, cudaStream_t stream) {
+  const bool wide = sel_wide(k);
+  switch (p.lpc) {
+    case 2:
+      return wide ? launch_sel<T, TD, 2, 1, true>(k, p, stream)
+                  : launch_sel<T, TD, 2, 1, false>(k, p, stream);
+    case 4:
+      if (p.r == 2)
+        return wide ? launch_sel<T, TD, 4, 2, true>(k, p, stream)
+                    : launch_sel<T, TD, 4, 2, false>(k, p, stream);
+      return wide ? launch_sel<T, TD, 4, 1, true>(k, p, stream)
+                  : launch_sel<T, TD, 4, 1, false>(k, p, stream);
+    case 8: return launch_sel<T, TD, 8, 2, false>(k, p, stream);
+    case 16: return launch_sel<T, TD, 16, 4, false>(k, p, stream);
+    default: return launch_sel<T, TD, 32, 8, false>(k, p, stream);
+  }
 }
 
 template <int LPC>
@@ -254,13 +302,17 @@ ssd_status launch_sel_step(const ssd::cache::SelArgs& k, cudaStream_t stream) {
 
 // ---- group norm --------------------------------------------------------------------------------
 
-// A variant of the norm kernels (LANES, NV, VW, threads) and its grid.
+// A variant of the norm kernels (LANES, NV, VW, threads) and its grid.  `vecs`: 16-byte pieces of
+// input per eight channels (they set the shared memory of a CTA's ring of rows).
 struct NormPlan {
-  int lanes, nv, vw, threads;
+  int lanes, nv, vw, threads, depth;
+  size_t smem;
   int64_t cta_rows, grid;
   bool ok;
 };
-NormPlan make_norm_plan(int64_t rows, int cdim, int ngroups, bool wide) {
+// Shared memory of a ring at most; with it and the fixed arrays a CTA stays below 227 KB.
+constexpr size_t kNormSmem = 192 * 1024;
+NormPlan make_norm_plan(int64_t rows, int cdim, int ngroups, bool wide, int vecs) {
   NormPlan p{};
   const int gs = cdim / ngroups;
   p.vw = wide ? 8 : 1;
@@ -278,11 +330,20 @@ NormPlan make_norm_plan(int64_t rows, int cdim, int ngroups, bool wide) {
     p.threads = ((units + p.nv - 1) / p.nv + 31) / 32 * 32;
     p.ok = p.threads <= 1024;
   }
+  p.depth = 1;
+  if (wide) {
+    const size_t row = size_t(p.nv) * vecs * p.threads * 16;
+    p.depth = int(std::max<size_t>(1, std::min<size_t>(ssd::norm::kDepth, kNormSmem / row)));
+    p.smem = p.depth * row;
+    p.ok = p.ok && p.smem <= kNormSmem;
+  }
   const int teams = p.lanes ? p.threads / p.lanes : 1;
   const int gpc = std::min(teams, ngroups), rpc = teams / gpc;
   const int64_t gblk = (ngroups + gpc - 1) / gpc;
-  const int64_t most = std::max<int64_t>(1, int64_t(sm_count()) * std::max(1, 1024 / p.threads) /
-                                                gblk);
+  // CTAs of an SM: about 1024 threads, and what the rings leave of its shared memory
+  const int64_t per_sm = std::max<int64_t>(
+      1, std::min<int64_t>(1024 / p.threads, 200 * 1024 / int64_t(p.smem + 4096)));
+  const int64_t most = std::max<int64_t>(1, sm_count() * per_sm / gblk);
   p.cta_rows = std::max<int64_t>(1, std::min((rows + rpc - 1) / rpc, most));
   p.grid = p.cta_rows * gblk;
   return p;
@@ -293,17 +354,39 @@ NormPlan make_norm_plan(int64_t rows, int cdim, int ngroups, bool wide) {
   X(0, 2, 8, 512) X(0, 2, 8, 1024) X(32, 1, 1, 128) X(32, 4, 1, 128) X(0, 4, 1, 512)          \
   X(0, 8, 1, 1024)
 
+// Lets a kernel use the SM's shared memory past 48 KB; once per kernel and device.
+bool allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done) {
+  if (bytes <= 48 * 1024) return true;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done->load() & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(kNormSmem)) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (dev < 64) done->fetch_or(bit);
+  return true;
+}
+
+template <typename K>
+ssd_status launch_norm_kernel(K kernel, const NormPlan& p, const ssd::norm::NormArgs& a,
+                              cudaStream_t stream, std::atomic<uint64_t>* done) {
+  if (!allow_smem(reinterpret_cast<const void*>(kernel), p.smem, done)) return SSD_ERR_CUDA;
+  kernel<<<unsigned(p.grid), p.threads, p.smem, stream>>>(a);
+  return launched();
+}
+
 ssd_status launch_norm(const NormPlan& p, const ssd::norm::NormArgs& a, bool bwd,
                        cudaStream_t stream) {
 #define X(L, NV, VW, MAXT)                                                                    \
   if (p.lanes == L && p.nv == NV && p.vw == VW && p.threads <= MAXT) {                        \
-    if (bwd)                                                                                  \
-      ssd::norm::group_norm_bwd_kernel<L, NV, VW, MAXT>                                       \
-          <<<unsigned(p.grid), p.threads, 0, stream>>>(a);                                    \
-    else                                                                                      \
-      ssd::norm::group_norm_kernel<L, NV, VW, MAXT>                                           \
-          <<<unsigned(p.grid), p.threads, 0, stream>>>(a);                                    \
-    return launched();                                                                        \
+    static std::atomic<uint64_t> done[2];                                                     \
+    return bwd ? launch_norm_kernel(ssd::norm::group_norm_bwd_kernel<L, NV, VW, MAXT>, p, a,  \
+                                    stream, &done[1])                                         \
+               : launch_norm_kernel(ssd::norm::group_norm_kernel<L, NV, VW, MAXT>, p, a,      \
+                                    stream, &done[0]);                                        \
   }
   SSD_NORM_VARIANTS(X)
 #undef X
@@ -374,13 +457,9 @@ ssd_status ssd_selective_scan_varlen(const ssd_selective_args* args, const int32
     k.ws_dt = reinterpret_cast<float*>(
         static_cast<char*>(workspace) + align256(size_t(p.units) * k.dim * k.dstate * 4));
   }
-  switch (p.lpc) {
-    case 2: return launch_sel<2, 1>(k, p, stream);
-    case 4: return p.r == 2 ? launch_sel<4, 2>(k, p, stream) : launch_sel<4, 1>(k, p, stream);
-    case 8: return launch_sel<8, 2>(k, p, stream);
-    case 16: return launch_sel<16, 4>(k, p, stream);
-    default: return launch_sel<32, 8>(k, p, stream);
-  }
+  if (!k.io_bf16) return launch_sel_shape<float, float>(k, p, stream);
+  if (k.dt_bf16) return launch_sel_shape<__nv_bfloat16, __nv_bfloat16>(k, p, stream);
+  return launch_sel_shape<__nv_bfloat16, float>(k, p, stream);
 }
 
 ssd_status ssd_selective_step(const ssd_selective_args* args, int64_t batch,
@@ -417,21 +496,23 @@ ssd_status ssd_group_norm_gate(const void* y, int64_t y_stride, const float* wei
   const bool wide = (cdim / ngroups) % 8 == 0 && rows16(y, y_stride, ey) && y_stride % 8 == 0 &&
                     (!z || (rows16(z, z_stride, ez) && z_stride % 8 == 0)) &&
                     rows16(out, out_stride, eo) && out_stride % 8 == 0;
-  const NormPlan p = make_norm_plan(rows, cdim, ngroups, wide);
-  if (!p.ok || p.grid > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   ssd::norm::NormArgs a{};
   a.y = y; a.z = z; a.w = weight; a.b = bias; a.out = out;
   a.ys = y_stride; a.zs = z_stride; a.os = out_stride;
   a.rows = rows; a.cdim = cdim; a.ngroups = ngroups; a.eps = eps;
   a.y_bf16 = y_dtype == SSD_BF16; a.z_bf16 = z_dtype == SSD_BF16; a.o_bf16 = out_dtype == SSD_BF16;
   a.center = center != 0; a.gate_first = gate_first != 0;
+  const NormPlan p = make_norm_plan(rows, cdim, ngroups, wide, ssd::norm::ring_vecs(a));
+  a.depth = p.depth;
+  if (!p.ok || p.grid > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   return launch_norm(p, a, false, stream);
 }
 
 size_t ssd_group_norm_gate_bwd_workspace_size(int64_t rows, int cdim, int ngroups) {
   if (!norm_shape_ok(rows, cdim, ngroups) || rows == 0) return 0;
-  const int64_t n = std::max(make_norm_plan(rows, cdim, ngroups, false).cta_rows,
-                             make_norm_plan(rows, cdim, ngroups, true).cta_rows);
+  int64_t n = make_norm_plan(rows, cdim, ngroups, false, 0).cta_rows;
+  for (int vecs = 2; vecs <= 6; ++vecs)  // whatever the types
+    n = std::max(n, make_norm_plan(rows, cdim, ngroups, true, vecs).cta_rows);
   return align256(size_t(n) * 2 * cdim * 4);
 }
 
@@ -465,19 +546,19 @@ ssd_status ssd_group_norm_gate_bwd(const void* dout, int64_t dout_stride, const 
   const bool wide = (cdim / ngroups) % 8 == 0 && rows16(y, y_stride, ey) && y_stride % 8 == 0 &&
                     (!z || (rows16(z, z_stride, ez) && z_stride % 8 == 0 && aligned16(dz))) &&
                     rows16(dout, dout_stride, eo) && dout_stride % 8 == 0 && aligned16(dy);
-  NormPlan p = make_norm_plan(rows, cdim, ngroups, wide);
+  ssd::norm::NormArgs a{};
+  a.y = y; a.z = z; a.w = weight; a.b = bias; a.dout = dout; a.dy = dy; a.dz = dz;
+  a.part = static_cast<float*>(workspace);
+  a.ys = y_stride; a.zs = z_stride; a.os = dout_stride;
+  a.rows = rows; a.cdim = cdim; a.ngroups = ngroups; a.eps = eps;
+  a.y_bf16 = y_dtype == SSD_BF16; a.z_bf16 = z_dtype == SSD_BF16; a.o_bf16 = dout_dtype == SSD_BF16;
+  a.center = center != 0; a.gate_first = gate_first != 0;
+  NormPlan p = make_norm_plan(rows, cdim, ngroups, wide, ssd::norm::ring_vecs(a));
+  a.depth = p.depth;
   if (!p.ok || p.grid > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   if (rows == 0) {
     p.cta_rows = 0;
   } else {
-    ssd::norm::NormArgs a{};
-    a.y = y; a.z = z; a.w = weight; a.b = bias; a.dout = dout; a.dy = dy; a.dz = dz;
-    a.part = static_cast<float*>(workspace);
-    a.ys = y_stride; a.zs = z_stride; a.os = dout_stride;
-    a.rows = rows; a.cdim = cdim; a.ngroups = ngroups; a.eps = eps;
-    a.y_bf16 = y_dtype == SSD_BF16; a.z_bf16 = z_dtype == SSD_BF16;
-    a.o_bf16 = dout_dtype == SSD_BF16;
-    a.center = center != 0; a.gate_first = gate_first != 0;
     const ssd_status st = launch_norm(p, a, true, stream);
     if (st != SSD_OK) return st;
   }

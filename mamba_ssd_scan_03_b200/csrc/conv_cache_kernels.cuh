@@ -18,16 +18,82 @@ namespace cache {
 // Sites of the latched status word (ssd_common.cuh) that these kernels use.
 constexpr unsigned kSiteSeq = 200, kSiteSlot = 201;
 
-// VW neighbouring channels of a row: one vector access, or element by element for VW = 1.
+// VW neighbouring channels of a row: one access of up to 16 bytes.
 template <typename T, int VW>
 __device__ __forceinline__ void load_ch(const T* p, float (&v)[VW]) {
-  if constexpr (VW == 1) v[0] = io_traits<T>::load(p, 0);
-  else glue::vec<T>::load(p, v);
+  if constexpr (VW == 1) {
+    v[0] = io_traits<T>::load(p, 0);
+  } else if constexpr (VW == 4) {
+    io_traits<T>::load4(p, 0, v);
+  } else if constexpr (sizeof(T) == 2) {  // VW == 2
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    v[0] = bf16lo(u);
+    v[1] = bf16hi(u);
+  } else {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    v[0] = f.x;
+    v[1] = f.y;
+  }
 }
 template <typename T, int VW>
 __device__ __forceinline__ void store_ch(T* p, const float (&v)[VW]) {
-  if constexpr (VW == 1) io_traits<T>::store(p, 0, v[0]);
-  else glue::vec<T>::store(p, v);
+  if constexpr (VW == 1) {
+    io_traits<T>::store(p, 0, v[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    if constexpr (VW == 4)
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+      *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+  } else {
+    if constexpr (VW == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  }
+}
+// The weights of VW neighbouring channels, VW * K values in a row.  VW > 1: w is 16-byte aligned
+// and the channel index a multiple of VW.
+template <int K, int VW>
+__device__ __forceinline__ void load_w(const float* w, float (&wr)[VW][K]) {
+  constexpr int kAt = (VW * K) % 4 == 0 ? 4 : (VW * K) % 2 == 0 ? 2 : 1;
+#pragma unroll
+  for (int i = 0; i < VW * K; i += kAt) {
+    float f[4];
+    if constexpr (VW > 1 && kAt == 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(w + i));
+      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else if constexpr (VW > 1 && kAt == 2) {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(w + i));
+      f[0] = v.x; f[1] = v.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < kAt; ++e) f[e] = __ldg(w + i + e);
+    }
+#pragma unroll
+    for (int e = 0; e < kAt; ++e) wr[(i + e) / K][(i + e) % K] = f[e];
+  }
+}
+// silu(b + sum_k w[k] win[k]) of VW channels, in float32 pairs where there are two.
+template <int K, int VW, int W>
+__device__ __forceinline__ void conv_silu_row(const float (&win)[W][VW], int first,
+                                              const float (&wr)[VW][K], const float (&bv)[VW],
+                                              float (&o)[VW]) {
+  if constexpr (VW == 1) {
+    float acc = bv[0];
+#pragma unroll
+    for (int k = 0; k < K; ++k) acc = fmaf(wr[0][k], win[first + k][0], acc);
+    o[0] = glue::silu_fast(acc);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VW; j += 2) {
+      float2 acc = make_float2(bv[j], bv[j + 1]);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        acc = fma2(make_float2(wr[j][k], wr[j + 1][k]),
+                   make_float2(win[first + k][j], win[first + k][j + 1]), acc);
+      const float2 t = mul2(acc, make_float2(-kLog2e, -kLog2e));
+      o[j] = __fdividef(acc.x, 1.f + ex2(t.x));
+      o[j + 1] = __fdividef(acc.y, 1.f + ex2(t.y));
+    }
+  }
 }
 
 // A warp's answer: the slot of sequence i, or -1 where the sequence is to be left alone: a
@@ -71,17 +137,16 @@ struct ConvArgs {
   T* out;
   int64_t us, os, ntok, nslots;  // row strides of u and out in elements
   int nseq, cdim;
+  int run;  // packed rows of a warp (prompts)
 };
 
-// Prompts.  One warp per (run of kRun packed rows, 32 groups of VW channels), a thread walking
+// Prompts.  One warp per (run of packed rows, 32 groups of VW channels), a thread walking
 // its channels down the rows as conv_silu_kernel does: weights and the window in registers,
 // STEP rows' loads in flight together.  Only where a run meets the start of a sequence does
 // the window restart.  A run that holds a sequence's first row owns the sequence's first K-1
 // rows even where they reach past the run (the rows that read the history), and moves the
 // history on itself after reading it: no other warp touches the slot, so the update in place
 // needs no second launch and no ordering between CTAs.
-constexpr int kRun = 64;
-
 template <typename T, int K, int VW, int STEP>
 __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
   constexpr int W = K - 1 + STEP;
@@ -90,8 +155,8 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
   const unsigned run = blockIdx.x / ncb, cb = blockIdx.x % ncb;
   const int c0 = int(cb * 32 + lane) * VW;
   const bool live = c0 < a.cdim;  // VW > 1 only where cdim is a multiple of VW
-  const int64_t r0 = int64_t(run) * kRun;
-  const int64_t r1 = r0 + kRun < a.ntok ? r0 + kRun : a.ntok;
+  const int64_t r0 = int64_t(run) * a.run;
+  const int64_t r1 = r0 + a.run < a.ntok ? r0 + a.run : a.ntok;
   const T* ub = a.u + c0;
   T* ob = a.out + c0;
 
@@ -128,12 +193,9 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
   }
 
   float wr[VW][K], bv[VW];
+  load_w<K, VW>(a.w + int64_t(live ? c0 : 0) * K, wr);
 #pragma unroll
-  for (int j = 0; j < VW; ++j) {
-    bv[j] = live && a.bias ? a.bias[c0 + j] : 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) wr[j][k] = live ? a.w[int64_t(c0 + j) * K + k] : 0.f;
-  }
+  for (int j = 0; j < VW; ++j) bv[j] = live && a.bias ? a.bias[c0 + j] : 0.f;
 
   for (int64_t r = r0; seq < a.nseq; ++seq) {
     const int64_t s = a.cu[seq], e0 = a.cu[seq + 1];
@@ -194,13 +256,7 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
         for (int i = 0; i < STEP; ++i) {
           if (t + i < end) {
             float o[VW];
-#pragma unroll
-            for (int j = 0; j < VW; ++j) {
-              float acc = bv[j];
-#pragma unroll
-              for (int k = 0; k < K; ++k) acc = fmaf(wr[j][k], win[i + k][j], acc);
-              o[j] = glue::silu_fast(acc);
-            }
+            conv_silu_row<K, VW>(win, i, wr, bv, o);
             store_ch<T, VW>(ob + (t + i) * a.os, o);
           }
         }
@@ -213,30 +269,44 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
   }
 }
 
-// One token of each sequence: a thread per (row, VW channels) reads its K-1 history rows and the
-// new one, writes the output and the moved history.
-template <typename T, int K, int VW>
+// One token of each sequence: a thread takes VW channels of RB rows, reads each row's K-1 history
+// rows and its new one, and writes the output and the moved history.  The weights are read once
+// for the RB rows.
+template <typename T, int K, int VW, int RB>
 __global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs<T> a) {
   const int c0 = int(blockIdx.y * blockDim.x + threadIdx.x) * VW;
-  const int64_t row = blockIdx.x;
-  const int64_t slot = warp_slot(a.slots, row, a.nslots);
-  if (slot < 0 || c0 >= a.cdim) return;
-  T* st = a.state + slot * (K - 1) * a.cdim + c0;
-  float win[K][VW];
+  const int64_t row0 = int64_t(blockIdx.x) * RB;
+  const bool live = c0 < a.cdim;
+  int64_t slot[RB];
+  float win[RB][K][VW];
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) load_ch<T, VW>(st + int64_t(k) * a.cdim, win[k]);
-  load_ch<T, VW>(a.u + row * a.us + c0, win[K - 1]);
-  float o[VW];
-#pragma unroll
-  for (int j = 0; j < VW; ++j) {
-    float acc = a.bias ? a.bias[c0 + j] : 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) acc = fmaf(a.w[int64_t(c0 + j) * K + k], win[k][j], acc);
-    o[j] = glue::silu_fast(acc);
+  for (int r = 0; r < RB; ++r) {
+    const int64_t row = row0 + r < a.ntok ? row0 + r : a.ntok - 1;
+    if (live) load_ch<T, VW>(a.u + row * a.us + c0, win[r][K - 1]);
   }
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) store_ch<T, VW>(st + int64_t(k) * a.cdim, win[k + 1]);
-  store_ch<T, VW>(a.out + row * a.os + c0, o);
+  for (int r = 0; r < RB; ++r) {
+    slot[r] = row0 + r < a.ntok ? warp_slot(a.slots, row0 + r, a.nslots) : -1;
+    if (!live || slot[r] < 0) continue;
+    const T* st = a.state + slot[r] * (K - 1) * a.cdim + c0;
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) load_ch<T, VW>(st + int64_t(k) * a.cdim, win[r][k]);
+  }
+  if (!live) return;
+  float wr[VW][K], bv[VW];
+  load_w<K, VW>(a.w + int64_t(c0) * K, wr);
+#pragma unroll
+  for (int j = 0; j < VW; ++j) bv[j] = a.bias ? a.bias[c0 + j] : 0.f;
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    if (slot[r] < 0) continue;
+    float o[VW];
+    conv_silu_row<K, VW>(win[r], 0, wr, bv, o);
+    T* st = a.state + slot[r] * (K - 1) * a.cdim + c0;
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) store_ch<T, VW>(st + int64_t(k) * a.cdim, win[r][k + 1]);
+    store_ch<T, VW>(a.out + (row0 + r) * a.os + c0, o);
+  }
 }
 
 }  // namespace cache

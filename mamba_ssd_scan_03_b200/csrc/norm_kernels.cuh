@@ -36,6 +36,7 @@ struct NormArgs {
   int64_t rows;
   int cdim, ngroups;
   float eps;
+  int depth;  // rows of the ring
   bool y_bf16, z_bf16, o_bf16, center, gate_first;
 };
 
@@ -128,12 +129,108 @@ struct Place {
 
 __device__ __forceinline__ float sigm(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
+// A thread's inputs of its next rows.  VW = 8: a ring of kDepth rows in shared memory that the
+// thread fills for itself with 16-byte asynchronous copies, so that the loads of later rows are in
+// flight while a row is worked on, and no barrier is needed.  VW = 1: plain loads.
+constexpr int kDepth = 3;  // at most; fewer where a CTA's rows are too long (NormArgs::depth)
+__host__ __device__ inline int ring_vecs(const NormArgs& a) {  // 16-byte pieces of 8 channels
+  return (a.y_bf16 ? 1 : 2) + (a.z ? (a.z_bf16 ? 1 : 2) : 0) + (a.dout ? (a.o_bf16 ? 1 : 2) : 0);
+}
+template <int LANES, int NV, int VW>
+__device__ __forceinline__ void norm_fill(const NormArgs& a, const Place<LANES, NV, VW>& p, int c0,
+                                          int64_t row, uint4* ring) {
+  if constexpr (VW == 8) {
+    if (p.on && row < a.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = p.col(i);
+        if (c >= p.gs) continue;
+        uint4* to = ring + i * ring_vecs(a) * blockDim.x;
+        auto copy = [&](const void* base, int64_t at, bool bf16) {
+          const char* from = static_cast<const char*>(base) + at * (bf16 ? 2 : 4);
+          for (int k = 0; k < (bf16 ? 1 : 2); ++k, to += blockDim.x)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             uint32_t(__cvta_generic_to_shared(to))),
+                         "l"(from + 16 * k)
+                         : "memory");
+        };
+        copy(a.y, row * a.ys + c0 + c, a.y_bf16);
+        if (a.z) copy(a.z, row * a.zs + c0 + c, a.z_bf16);
+        if (a.dout) copy(a.dout, row * a.os + c0 + c, a.o_bf16);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+}
+// y, z and dout of unit i of the row that the ring's oldest stage holds (zeros off the end).
+template <int LANES, int NV, int VW>
+__device__ __forceinline__ void norm_take(const NormArgs& a, const Place<LANES, NV, VW>& p, int c0,
+                                          int64_t row, const uint4* ring, int i, float (&y)[VW],
+                                          float (&z)[VW], float (&d)[VW]) {
+  const int c = p.col(i);
+  const bool in = p.on && row < a.rows && c < p.gs;
+#pragma unroll
+  for (int j = 0; j < VW; ++j) y[j] = z[j] = d[j] = 0.f;
+  if (!in) return;
+  if constexpr (VW == 8) {
+    const uint4* from = ring + i * ring_vecs(a) * blockDim.x;
+    auto take = [&](float (&v)[VW], bool bf16) {
+      const uint4 u = *from;
+      from += blockDim.x;
+      if (bf16) {
+        v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
+        v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
+      } else {
+        const uint4 t = *from;
+        from += blockDim.x;
+        v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+        v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+        v[4] = __uint_as_float(t.x); v[5] = __uint_as_float(t.y);
+        v[6] = __uint_as_float(t.z); v[7] = __uint_as_float(t.w);
+      }
+    };
+    take(y, a.y_bf16);
+    if (a.z) take(z, a.z_bf16);
+    if (a.dout) take(d, a.o_bf16);
+  } else {
+    load_n<VW>(a.y, row * a.ys + c0 + c, a.y_bf16, y);
+    if (a.z) load_n<VW>(a.z, row * a.zs + c0 + c, a.z_bf16, z);
+    if (a.dout) load_n<VW>(a.dout, row * a.os + c0 + c, a.o_bf16, d);
+  }
+}
+// The rows of a CTA: row(k) is handed on with its ring stage when its copies have landed.
+template <int LANES, int NV, int VW, typename F>
+__device__ __forceinline__ void norm_rows(const NormArgs& a, const Place<LANES, NV, VW>& p, int c0,
+                                          uint4* ring, const F& each) {
+  const int per = VW == 8 ? NV * ring_vecs(a) * int(blockDim.x) : 0;  // of a stage
+  ring += threadIdx.x;
+  int in = 0, par = 0;
+  int64_t ahead = p.row;
+  for (; in < a.depth - 1; ++in, ahead += p.step) norm_fill(a, p, c0, ahead, ring + in * per);
+  int at = 0;
+  // every team of a CTA runs the same number of rounds: the sums are collective
+  for (int64_t r0 = 0; r0 < a.rows; r0 += p.step, ahead += p.step, par ^= 1) {
+    norm_fill(a, p, c0, ahead, ring + in * per);
+    in = in + 1 == a.depth ? 0 : in + 1;
+    if constexpr (VW == 8) {  // all but the depth - 1 youngest rows have landed
+      if (a.depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (a.depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    each(r0 + p.row, ring + at * per, par);
+    at = at + 1 == a.depth ? 0 : at + 1;
+  }
+  if constexpr (VW == 8) asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // Threads of a CTA: 128 in teams of lanes, at most MAXT as one team (which bounds the registers).
 template <int LANES, int NV, int VW, int MAXT>
 __global__ void __launch_bounds__(MAXT) group_norm_kernel(const NormArgs a) {
-  __shared__ float buf[2][2][2][32];
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float buf[2][2][1][32];
   const Place<LANES, NV, VW> p(a);
   const int c0 = p.group * p.gs;
+  const float inv = 1.f / p.gs;
   float w[NV][VW], bb[NV][VW];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -141,35 +238,22 @@ __global__ void __launch_bounds__(MAXT) group_norm_kernel(const NormArgs a) {
     for (int j = 0; j < VW; ++j) {
       const int c = p.col(i) + j;
       const bool in = p.on && c < p.gs;
-      w[i][j] = in ? a.w[c0 + c] : 0.f;
-      bb[i][j] = in && a.b ? a.b[c0 + c] : 0.f;
+      w[i][j] = in ? __ldg(a.w + c0 + c) : 0.f;
+      bb[i][j] = in && a.b ? __ldg(a.b + c0 + c) : 0.f;
     }
-  const float inv = 1.f / p.gs;
-  // every team of a CTA runs the same number of rounds: the sums are collective
-  int par = 0;
-  for (int64_t r0 = 0; r0 < a.rows; r0 += p.step, par ^= 1) {
-    const int64_t row = r0 + p.row;
+  norm_rows(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
     const bool live = p.on && row < a.rows;
-    float v[NV][VW], zv[NV][VW];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = p.col(i);
-      if (live && c < p.gs) {
-        load_n<VW>(a.y, row * a.ys + c0 + c, a.y_bf16, v[i]);
-        if (a.z) load_n<VW>(a.z, row * a.zs + c0 + c, a.z_bf16, zv[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VW; ++j) v[i][j] = zv[i][j] = 0.f;
-      }
-    }
+    float v[NV][VW], zv[NV][VW], none[VW];
     float s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      norm_take(a, p, c0, row, st, i, v[i], zv[i], none);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         if (a.z && a.gate_first) v[i][j] *= glue::silu_fast(zv[i][j]);
         s[0] += v[i][j];
       }
+    }
     float mu = 0.f;
     if (a.center) {
       team_sum<LANES>(s, buf[par][0]);
@@ -198,11 +282,12 @@ __global__ void __launch_bounds__(MAXT) group_norm_kernel(const NormArgs a) {
         store_n<VW>(a.out, row * a.os + c0 + c, a.o_bf16, o);
       }
     }
-  }
+  });
 }
 
 template <int LANES, int NV, int VW, int MAXT>
 __global__ void __launch_bounds__(MAXT) group_norm_bwd_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float buf[2][2][3][32];
   Place<LANES, NV, VW> p(a);
   const int c0 = p.group * p.gs;
@@ -212,28 +297,16 @@ __global__ void __launch_bounds__(MAXT) group_norm_bwd_kernel(const NormArgs a) 
 #pragma unroll
     for (int j = 0; j < VW; ++j) {
       const int c = p.col(i) + j;
-      w[i][j] = p.on && c < p.gs ? a.w[c0 + c] : 0.f;
+      w[i][j] = p.on && c < p.gs ? __ldg(a.w + c0 + c) : 0.f;
       dw[i][j] = db[i][j] = 0.f;
     }
   const float inv = 1.f / p.gs;
   const bool first = a.z && a.gate_first, gate_last = a.z && !a.gate_first;
-  int par = 0;
-  for (int64_t r0 = 0; r0 < a.rows; r0 += p.step, par ^= 1) {
-    const int64_t row = r0 + p.row;
+  norm_rows(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
     const bool live = p.on && row < a.rows;
     float y[NV][VW], z[NV][VW], d[NV][VW];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = p.col(i);
-      if (live && c < p.gs) {
-        load_n<VW>(a.y, row * a.ys + c0 + c, a.y_bf16, y[i]);
-        load_n<VW>(a.dout, row * a.os + c0 + c, a.o_bf16, d[i]);
-        if (a.z) load_n<VW>(a.z, row * a.zs + c0 + c, a.z_bf16, z[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VW; ++j) y[i][j] = z[i][j] = d[i][j] = 0.f;
-      }
-    }
+    for (int i = 0; i < NV; ++i) norm_take(a, p, c0, row, st, i, y[i], z[i], d[i]);
     float mu = 0.f;
     if (a.center) {
       float s[1] = {0.f};
@@ -284,7 +357,7 @@ __global__ void __launch_bounds__(MAXT) group_norm_bwd_kernel(const NormArgs a) 
         if (a.z) store_n<VW>(a.dz, row * int64_t(a.cdim) + c0 + c, a.z_bf16, odz);
       }
     }
-  }
+  });
   // one row of partial sums per CTA; the teams of one group add theirs in turn
   const int per = a.b ? 2 : 1;
   float* to = a.part + int64_t(p.cta_row) * per * a.cdim + c0;

@@ -49,16 +49,56 @@ __device__ __forceinline__ float rate2(float a) {
   return r < -1e38f ? -1e38f : r;
 }
 
-// softplus(v) = max(v, 0) + log(1 + e^-|v|): no exponential overflows, and small results keep
-// their relative accuracy through log1p.
+// softplus(v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1]: no exponential overflows, and
+// small results keep their relative accuracy: log(1 + e) = 2 atanh(w), w = e / (2 + e) <= 1/3,
+// by the odd series w + w^3/3 + w^5/5 + ...; the terms past w^13 / 13 are below 2^-25 of it.
 __device__ __forceinline__ float softplus_acc(float v) {
-  return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+  const float e = ex2(-fabsf(v) * kLog2e);
+  const float w = __fdividef(e, 2.f + e), s = w * w;
+  float p = fmaf(s, 1.f / 13.f, 1.f / 11.f);
+  p = fmaf(s, p, 1.f / 9.f);
+  p = fmaf(s, p, 1.f / 7.f);
+  p = fmaf(s, p, 1.f / 5.f);
+  p = fmaf(s, p, 1.f / 3.f);
+  const float w2 = w + w;
+  return fmaxf(v, 0.f) + fmaf(w2 * s, p, w2);
 }
 
 __device__ __forceinline__ float load_any(const void* p, int64_t i, bool bf16) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
               : static_cast<const float*>(p)[i];
 }
+
+// NV neighbouring values of a row as they lie in memory (one or two wide accesses), or one value
+// per word.  Loading and converting are kept apart, and nothing branches between a load and the
+// stage that converts it: a value is first waited for there.
+template <typename T, int NV, bool VEC>
+struct Raw {
+  static constexpr int kWords = VEC ? NV * int(sizeof(T)) / 4 : NV;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {  // VEC
+    const unsigned char* q = reinterpret_cast<const unsigned char*>(p);
+    if constexpr (kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kWords / 4; ++k) {
+        const uint4 v = reinterpret_cast<const uint4*>(q)[k];
+        w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void load1(int i, const T* p) {  // one value per word
+    if constexpr (sizeof(T) == 2) w[i] = *reinterpret_cast<const unsigned short*>(p);
+    else w[i] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (VEC) return (i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+    else return bf16lo(w[i]);
+  }
+};
 
 // LPC lanes per channel, each holding 4 of its (up to 4 LPC) states; R channels per lane.
 template <int LPC, int R>
@@ -67,12 +107,19 @@ struct SelShape {
   static constexpr int kCh = kCg * R;          // channels of a warp
   static constexpr int kNp = LPC * 4;          // states, padded
   static constexpr int kTok = LPC <= 4 ? 16 : 8;  // tokens staged together
-  static constexpr int kDu = 2 * kCh + 4;      // floats per staged row of (dt, dt x) pairs
-  static constexpr int kY = kCh + 8;           // and of y
+  static constexpr int kDu = 2 * kCh;          // floats per staged row of (dt, dt x) pairs
+  static constexpr int kPp = LPC < 4 ? LPC : 4;  // partial sums of y per channel
+  static constexpr int kY = kPp * kCh;         // floats per row of them
   static constexpr int kEx = kTok * kCh / 32;  // x, dt, z elements per lane and stage
   static constexpr int kEb = kTok * kNp / 32;  // B, C elements per lane and stage
-  static constexpr int kFloats = kTok * (kDu + 2 * kNp + kY);
   static_assert(kTok * kCh % 32 == 0 && 32 % kCh == 0, "whole rows per step of the warp");
+  // Place of channel c's partial sums in the row of token t, in floats.  The four-way exchange
+  // with t puts what the lanes of a quarter warp read together (the same channels of four
+  // rows) on banks of their own.
+  static __device__ __forceinline__ int part(int t, int c) {
+    if constexpr (LPC == 2) return ((c >> 1) ^ (t & 3)) * 4 + (c & 1) * 2;
+    else return (c ^ (t & 3)) * 4;
+  }
 };
 
 // One warp scans one unit: a sequence (chunk == 0) or a chunk of one, for kCh channels of one
@@ -82,17 +129,15 @@ struct SelShape {
 //
 // Inputs come in stages of kTok tokens: the next stage's loads are issued into registers ahead
 // of the current stage's steps, then converted (softplus, dt x, D x) once per element into
-// shared memory, where the lanes of a channel all read them.  Neighbouring lanes load
-// neighbouring channels element by element, so no alignment is asked of the rows.
-template <int LPC, int R, bool SUMMARY>
+// shared memory, where the lanes of a channel all read them.  VEC: a lane loads kEx neighbouring
+// channels of one row (and kEb neighbouring states) in one access, which asks for rows of 16-byte
+// multiples; else neighbouring lanes load neighbouring channels one by one.
+template <typename T, typename TD, int LPC, int R, bool VEC, bool SUMMARY>
 __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
   using S = SelShape<LPC, R>;
-  constexpr int TK = S::kTok, CH = S::kCh, NP = S::kNp;
-  __shared__ __align__(16) float sm[S::kFloats];
-  float* du = sm;
-  float* bsm = du + TK * S::kDu;
-  float* csm = bsm + TK * NP;
-  float* ysm = csm + TK * NP;
+  constexpr int TK = S::kTok, CH = S::kCh, NP = S::kNp, EX = S::kEx, EB = S::kEb;
+  // arrays of their own, so that the compiler may move a token's loads over the stores before it
+  __shared__ __align__(16) float du[TK * S::kDu], bsm[TK * NP], csm[TK * NP], ysm[TK * S::kY];
 
   const int lane = threadIdx.x;
   const int dpg = a.dim / a.ngroups;
@@ -187,52 +232,148 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
   const int64_t t0 = s0 + int64_t(chunk) * a.chunk;
   const int64_t t1 = a.chunk && t0 + a.chunk < s1 ? t0 + a.chunk : s1;
 
-  // staging: element e = i * 32 + lane of a stage's [TK][CH] (or [TK][NP]) tile
-  const int ec = lane % CH, et = lane / CH;  // channel and first token row of x, dt, z, y
-  const bool eon = ec < nch;
-  const float Dd = eon && a.D ? a.D[d0 + ec] : 0.f;
-  const float bias = eon && a.dt_bias ? a.dt_bias[d0 + ec] : 0.f;
-  constexpr int kRows = 32 / CH;  // token rows per step of the warp
-  float rx[S::kEx], rd[S::kEx], rz[S::kEx], zc[S::kEx], rb[S::kEb], rc[S::kEb];
+  // staging: the rows and channels of this lane's elements of a stage's tiles
+  constexpr int kLr = CH / EX;  // VEC: lanes per row
+  auto row = [&](int i) { return VEC ? lane / kLr : lane / CH + i * (32 / CH); };
+  auto chn = [&](int i) { return VEC ? lane % kLr * EX + i : lane % CH; };
+  const bool eon = chn(0) < nch;
+  float Dd[EX], bias[EX];
+#pragma unroll
+  for (int i = 0; i < EX; ++i) {
+    Dd[i] = !SUMMARY && eon && a.D ? a.D[d0 + chn(i)] : 0.f;
+    bias[i] = eon && a.dt_bias ? a.dt_bias[d0 + chn(i)] : 0.f;
+  }
+  const T* px = static_cast<const T*>(a.x);
+  const TD* pt = static_cast<const TD*>(a.dt);
+  const T* pz = static_cast<const T*>(a.z);
+  const T* pb = static_cast<const T*>(a.B);
+  const T* pc = static_cast<const T*>(a.C);
+  Raw<T, EX, VEC> rx, rz, zc;
+  Raw<TD, EX, VEC> rd;
+  Raw<T, EB, VEC> rb, rc;
+  float skip[EX];  // D x of the staged tokens
+  // Rows past the end and channels or states past the last read the last one again, and are
+  // masked where they are staged.
   auto load = [&](int64_t t) {
+    if constexpr (VEC) {
+      const int64_t tt = min(t + row(0), t1 - 1);
+      const int c = d0 + (eon ? chn(0) : 0);
+      rx.load(px + tt * a.xs + c);
+      rd.load(pt + tt * a.dts + c);
+      if (!SUMMARY && pz) rz.load(pz + tt * a.zs + c);
+      constexpr int kLb = NP / EB;  // lanes per row of B and C
+      const int64_t tb = min(t + lane / kLb, t1 - 1);
+      const int n = g * N + lane % kLb * EB;
+      rb.load(pb + tb * a.bs + n);
+      if (!SUMMARY) rc.load(pc + tb * a.cs + n);
+    } else {
 #pragma unroll
-    for (int i = 0; i < S::kEx; ++i) {
-      const int64_t tt = t + et + i * kRows;
-      const bool on = eon && tt < t1;
-      rx[i] = on ? load_any(a.x, tt * a.xs + d0 + ec, a.io_bf16) : 0.f;
-      rd[i] = on ? load_any(a.dt, tt * a.dts + d0 + ec, a.dt_bf16) : 0.f;
-      if (!SUMMARY) rz[i] = on && a.z ? load_any(a.z, tt * a.zs + d0 + ec, a.io_bf16) : 0.f;
-    }
+      for (int i = 0; i < EX; ++i) {
+        const int64_t tt = min(t + row(i), t1 - 1);
+        const int c = d0 + (eon ? chn(i) : 0);
+        rx.load1(i, px + tt * a.xs + c);
+        rd.load1(i, pt + tt * a.dts + c);
+        if (!SUMMARY && pz) rz.load1(i, pz + tt * a.zs + c);
+      }
 #pragma unroll
-    for (int i = 0; i < S::kEb; ++i) {
-      const int e = i * 32 + lane, n = e % NP;
-      const int64_t tt = t + e / NP;
-      const bool on = n < N && tt < t1;
-      rb[i] = on ? load_any(a.B, tt * a.bs + int64_t(g) * N + n, a.io_bf16) : 0.f;
-      if (!SUMMARY) rc[i] = on ? load_any(a.C, tt * a.cs + int64_t(g) * N + n, a.io_bf16) : 0.f;
+      for (int i = 0; i < EB; ++i) {
+        const int e = i * 32 + lane;
+        const int64_t tb = min(t + e / NP, t1 - 1);
+        const int n = g * N + min(e % NP, N - 1);
+        rb.load1(i, pb + tb * a.bs + n);
+        if (!SUMMARY) rc.load1(i, pc + tb * a.cs + n);
+      }
     }
   };
   auto stage = [&](int64_t t) {
+    float xv[EX], dv[EX], bv[EB], cv[EB];
 #pragma unroll
-    for (int i = 0; i < S::kEx; ++i) {
-      const int row = et + i * kRows;
-      float dt = rd[i] + bias;
-      if (a.softplus) dt = softplus_acc(dt);
-      const bool on = t + row < t1;  // rows past the end are identity steps
-      *reinterpret_cast<float2*>(du + row * S::kDu + 2 * ec) =
-          on ? make_float2(dt, dt * rx[i]) : make_float2(0.f, 0.f);
-      if (!SUMMARY) {
-        ysm[row * S::kY + ec] = Dd * rx[i];
-        zc[i] = rz[i];
+    for (int i = 0; i < EX; ++i) {
+      const bool on = eon && t + row(i) < t1;  // a row past the end is an identity step
+      xv[i] = on ? rx.get(i) : 0.f;
+      dv[i] = rd.get(i) + bias[i];
+      if (a.softplus) dv[i] = softplus_acc(dv[i]);
+      if (!on) dv[i] = 0.f;
+      skip[i] = Dd[i] * xv[i];
+    }
+    zc = rz;
+#pragma unroll
+    for (int i = 0; i < EB; ++i) {
+      const int e = VEC ? lane * EB + i : i * 32 + lane;
+      const bool on = e % NP < N && t + e / NP < t1;
+      bv[i] = on ? rb.get(i) : 0.f;
+      if (!SUMMARY) cv[i] = on ? rc.get(i) : 0.f;
+    }
+    if constexpr (VEC) {
+      float4* pd = reinterpret_cast<float4*>(du + row(0) * S::kDu + 2 * chn(0));
+      float4* sb = reinterpret_cast<float4*>(bsm + lane * EB);
+      float4* sc = reinterpret_cast<float4*>(csm + lane * EB);
+#pragma unroll
+      for (int i = 0; i < EX; i += 2)
+        pd[i / 2] = make_float4(dv[i], dv[i] * xv[i], dv[i + 1], dv[i + 1] * xv[i + 1]);
+#pragma unroll
+      for (int i = 0; i < EB; i += 4) {
+        sb[i / 4] = make_float4(bv[i], bv[i + 1], bv[i + 2], bv[i + 3]);
+        if (!SUMMARY) sc[i / 4] = make_float4(cv[i], cv[i + 1], cv[i + 2], cv[i + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EX; ++i) {
+        *reinterpret_cast<float2*>(du + row(i) * S::kDu + 2 * chn(i)) =
+            make_float2(dv[i], dv[i] * xv[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < EB; ++i) {
+        bsm[i * 32 + lane] = bv[i];
+        if (!SUMMARY) csm[i * 32 + lane] = cv[i];
       }
     }
+  };
+  auto finish = [&](int64_t t) {  // y of a stage: the gate, the output's type
+    float v[EX];
 #pragma unroll
-    for (int i = 0; i < S::kEb; ++i) {
-      bsm[i * 32 + lane] = rb[i];
-      if (!SUMMARY) csm[i * 32 + lane] = rc[i];
+    for (int i = 0; i < EX; ++i) {
+      const float* pp = ysm + row(i) * S::kY + S::part(row(i), chn(i));
+      if constexpr (LPC == 2) {
+        const float2 f = *reinterpret_cast<const float2*>(pp);
+        v[i] = skip[i] + (f.x + f.y);
+      } else {
+        const float4 f = *reinterpret_cast<const float4*>(pp);
+        v[i] = skip[i] + ((f.x + f.y) + (f.z + f.w));
+      }
+      if (pz) v[i] *= glue::silu_fast(zc.get(i));
+    }
+    if constexpr (VEC) {
+      if (eon && t + row(0) < t1) {
+        const int64_t at = (t + row(0)) * a.ys + d0 + chn(0);
+        if (a.y_bf16) {
+          uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.y) + at);
+          if constexpr (EX == 4)
+            *reinterpret_cast<uint2*>(to) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          else
+            *reinterpret_cast<uint4*>(to) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        } else {
+          float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
+#pragma unroll
+          for (int i = 0; i < EX; i += 4)
+            to[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EX; ++i) {
+        if (!eon || t + row(i) >= t1) continue;
+        const int64_t at = (t + row(i)) * a.ys + d0 + chn(i);
+        if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v[i]);
+        else static_cast<float*>(a.y)[at] = v[i];
+      }
     }
   };
 
+  constexpr int kGroup = 4;
   if (t0 < t1) {
     load(t0);
     stage(t0);
@@ -240,71 +381,71 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
   __syncwarp();
   for (int64_t t = t0; t < t1; t += TK) {
     if (t + TK < t1) load(t + TK);
-    const int steps = t1 - t < TK ? int((t1 - t + 3) / 4) : TK / 4;
-    for (int k4 = 0; k4 < steps; ++k4) {
-      float pv[R][4];
+    const int steps = t1 - t < TK ? int((t1 - t + kGroup - 1) / kGroup) : TK / kGroup;
+    // kGroup tokens at a time, the next ones' operands on their way while these are worked on
+    float4 bn[kGroup], cn[kGroup];
+    float2 dn[kGroup][R];
+    auto fetch = [&](int k0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = k4 * 4 + i;
-        const float4 bv = *reinterpret_cast<const float4*>(bsm + row * NP + q * 4);
-        float4 cv;
-        if (!SUMMARY) cv = *reinterpret_cast<const float4*>(csm + row * NP + q * 4);
+      for (int i = 0; i < kGroup; ++i) {
+        bn[i] = *reinterpret_cast<const float4*>(bsm + (k0 + i) * NP + q * 4);
+        if (!SUMMARY) cn[i] = *reinterpret_cast<const float4*>(csm + (k0 + i) * NP + q * 4);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          dn[i][r] =
+              *reinterpret_cast<const float2*>(du + (k0 + i) * S::kDu + 2 * (cg * R + r));
+      }
+    };
+    fetch(0);
+    for (int k4 = 0; k4 < steps; ++k4) {
+      float4 bv[kGroup], cv[kGroup];
+      float2 dv[kGroup][R];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        bv[i] = bn[i];
+        if (!SUMMARY) cv[i] = cn[i];
+#pragma unroll
+        for (int r = 0; r < R; ++r) dv[i][r] = dn[i][r];
+      }
+      if (k4 + 1 < steps) fetch((k4 + 1) * kGroup);
+      float pv[kGroup][R];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float2 v =
-              *reinterpret_cast<const float2*>(du + row * S::kDu + 2 * (cg * R + r));
-          const float2 dd = make_float2(v.x, v.x), uu = make_float2(v.y, v.y);
+          const float2 dd = make_float2(dv[i][r].x, dv[i][r].x);
+          const float2 uu = make_float2(dv[i][r].y, dv[i][r].y);
           const float2 l01 = mul2(dd, a01[r]), l23 = mul2(dd, a23[r]);
           h01[r] = fma2(make_float2(ex2(l01.x), ex2(l01.y)), h01[r],
-                        mul2(uu, make_float2(bv.x, bv.y)));
+                        mul2(uu, make_float2(bv[i].x, bv[i].y)));
           h23[r] = fma2(make_float2(ex2(l23.x), ex2(l23.y)), h23[r],
-                        mul2(uu, make_float2(bv.z, bv.w)));
+                        mul2(uu, make_float2(bv[i].z, bv[i].w)));
           if (SUMMARY) {
-            sdt[r] += v.x;
+            sdt[r] += dd.x;
           } else {
-            const float2 p = fma2(make_float2(cv.z, cv.w), h23[r],
-                                  mul2(make_float2(cv.x, cv.y), h01[r]));
-            pv[r][i] = p.x + p.y;
+            const float2 p2 = fma2(make_float2(cv[i].z, cv[i].w), h23[r],
+                                   mul2(make_float2(cv[i].x, cv[i].y), h01[r]));
+            pv[i][r] = p2.x + p2.y;
           }
         }
       }
       if (!SUMMARY) {
-        // sum over the channel's lanes; with four lanes or more the four tokens are scattered
-        // over them (lane q ends with token q mod 4), with two each ends with two tokens
-        const int b0 = q & 1, b1 = (q >> 1) & 1;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float r0 = __shfl_xor_sync(0xffffffffu, b0 ? pv[r][0] : pv[r][1], 1);
-          const float k0 = (b0 ? pv[r][1] : pv[r][0]) + r0;  // token b0
-          const float r1 = __shfl_xor_sync(0xffffffffu, b0 ? pv[r][2] : pv[r][3], 1);
-          const float k1 = (b0 ? pv[r][3] : pv[r][2]) + r1;  // token 2 + b0
-          float* yr = ysm + k4 * 4 * S::kY + cg * R + r;
-          if constexpr (LPC == 2) {
-            yr[b0 * S::kY] += k0;
-            yr[(2 + b0) * S::kY] += k1;
-          } else {
-            const float r2 = __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2);
-            float yq = (b1 ? k1 : k0) + r2;
+        for (int i = 0; i < kGroup; ++i)
 #pragma unroll
-            for (int o = 4; o < LPC; o <<= 1) yq += __shfl_xor_sync(0xffffffffu, yq, o);
-            if (LPC == 4 || q < 4) yr[(q & 3) * S::kY] += yq;
+          for (int r = 0; r < R; ++r) {
+            float p = pv[i][r];
+#pragma unroll
+            for (int o = 4; o < LPC; o <<= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+            // the lanes' sums meet in shared memory, added when the stage's y is finished
+            if (LPC <= 4 || q < 4)
+              ysm[(k4 * kGroup + i) * S::kY + S::part(i, cg * R + r) + q] = p;
           }
-        }
       }
     }
     __syncwarp();
     if (!SUMMARY) {
-#pragma unroll
-      for (int i = 0; i < S::kEx; ++i) {
-        const int row = et + i * kRows;
-        if (eon && t + row < t1) {
-          float v = ysm[row * S::kY + ec];
-          if (a.z) v *= glue::silu_fast(zc[i]);
-          const int64_t at = (t + row) * a.ys + d0 + ec;
-          if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-          else static_cast<float*>(a.y)[at] = v;
-        }
-      }
+      finish(t);
       __syncwarp();
     }
     if (t + TK < t1) stage(t + TK);
