@@ -589,17 +589,19 @@ def _first(t, name, ndim):
     return t.get_device()
 
 
-def _empty(shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+# The raw handle of a device's current stream: a small call's time is largely its host time, and
+# building a Stream object for the handle alone costs 3 us of it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _launch(fn, dev, *args):
     """Call a C entry with device `dev` current, on its current stream."""
     if torch.cuda.current_device() == dev:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+        rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+            rc = fn(*args, _raw_stream(dev))
     if rc != 0:
         raise SSDError(rc, fn.__name__)
 
@@ -653,7 +655,7 @@ def conv_silu_varlen(u, w, cu_seqlens, bias=None, conv_state=None, slots=None, r
     nseq, cu, res = _seqs(cu_seqlens, resume, dev)
     state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
     if out is None:
-        out = _empty((T, Cd), u.dtype, dev)
+        out = u.new_empty((T, Cd))
     os_ = _row_stride(out, "out", u.dtype, (T, Cd), dev)
     _launch(load().ssd_conv_silu_varlen, dev, u.data_ptr(), us,
             _whole(w, "w", torch.float32, (Cd, K), dev),
@@ -673,7 +675,7 @@ def conv_silu_step(conv_state, u, w, bias=None, slots=None, out=None):
     us = _row_stride(u, "u", None, (Bt, Cd), dev)
     state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
     if out is None:
-        out = _empty((Bt, Cd), u.dtype, dev)
+        out = u.new_empty((Bt, Cd))
     os_ = _row_stride(out, "out", u.dtype, (Bt, Cd), dev)
     _launch(load().ssd_conv_silu_step, dev, state, u.data_ptr(), us,
             _whole(w, "w", torch.float32, (Cd, K), dev),
@@ -698,24 +700,24 @@ def _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, nseq,
         raise TypeError(f"dt must be float32 or {x.dtype}, got {dt.dtype}")
     shape, bc = (rows, dim), (rows, G, N)
     y_dtype = out.dtype if out is not None else y_dtype
-    y = _empty(shape, y_dtype, dev) if out is None else out
+    y = x.new_empty(shape, dtype=y_dtype) if out is None else out
     nslots = 0
     if state is not None:
         if not isinstance(state, torch.Tensor) or state.dim() != 3:
             raise ValueError("state must be a tensor [nslots, dim, dstate]")
         nslots = state.shape[0]
+    strides = (_row_stride(x, "x", None, shape, dev), _row_stride(dt, "dt", None, shape, dev),
+               _row_stride(B, "B", x.dtype, bc, dev), _row_stride(C, "C", x.dtype, bc, dev),
+               0 if z is None else _row_stride(z, "z", x.dtype, shape, dev),
+               _row_stride(y, "out", y_dtype, shape, dev))
     args = SelectiveArgs(
         x.data_ptr(), dt.data_ptr(), _whole(A, "A", torch.float32, (dim, N), dev), B.data_ptr(),
         C.data_ptr(), _whole(D, "D", torch.float32, (dim,), dev),
         _whole(dt_bias, "dt_bias", torch.float32, (dim,), dev),
         None if z is None else z.data_ptr(), y.data_ptr(),
         _whole(state, "state", torch.float32, (nslots, dim, N), dev),
-        _whole(slots, "slots", torch.int32, (nseq,), dev),
-        _row_stride(x, "x", None, shape, dev), _row_stride(dt, "dt", None, shape, dev),
-        _row_stride(B, "B", x.dtype, bc, dev), _row_stride(C, "C", x.dtype, bc, dev),
-        0 if z is None else _row_stride(z, "z", x.dtype, shape, dev),
-        _row_stride(y, "out", y_dtype, shape, dev), nslots, dim, N, G, io, _code(dt.dtype),
-        _code(y_dtype), 1 if softplus else 0)
+        _whole(slots, "slots", torch.int32, (rows if nseq is None else nseq,), dev), *strides,
+        nslots, dim, N, G, io, _code(dt.dtype), _code(y_dtype), 1 if softplus else 0)
     return dev, args, y
 
 
@@ -746,7 +748,7 @@ def selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=No
         _need(workspace, "workspace", torch.uint8, device=x.device)
         ws, need = workspace.data_ptr(), workspace.numel()
     elif need > 0:
-        workspace = _empty((need,), torch.uint8, dev)
+        workspace = x.new_empty((need,), dtype=torch.uint8)
         ws = workspace.data_ptr()
     _launch(lib.ssd_selective_scan_varlen, dev, ctypes.byref(args), cu, res, T, nseq, max_seqlen,
             ws, need)
@@ -757,8 +759,8 @@ def selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus
                    slots=None, out=None, y_dtype=torch.float32):
     """selective_scan_varlen for one token of each sequence: x, dt, z [batch,dim], B, C
     [batch,G,N]; state [nslots,dim,N] f32 is updated in place at each row's slot."""
-    dev, args, y = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots,
-                                   x.shape[0], out, y_dtype)
+    dev, args, y = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, None,
+                                   out, y_dtype)
     _launch(load().ssd_selective_step, dev, ctypes.byref(args), x.shape[0])
     return y
 
@@ -776,13 +778,12 @@ def group_norm_gate(y, weight, bias=None, z=None, ngroups=1, eps=1e-5, center=Fa
     shape = (rows, Cd)
     out_dtype = out.dtype if out is not None else out_dtype
     if out is None:
-        out = _empty(shape, out_dtype, dev)
+        out = y.new_empty(shape, dtype=out_dtype)
+    zs = 0 if z is None else _row_stride(z, "z", None, shape, dev)
+    os_ = _row_stride(out, "out", out_dtype, shape, dev)
     _launch(load().ssd_group_norm_gate, dev, y.data_ptr(), _row_stride(y, "y", None, shape, dev),
             _whole(weight, "weight", torch.float32, (Cd,), dev),
-            _whole(bias, "bias", torch.float32, (Cd,), dev),
-            None if z is None else z.data_ptr(),
-            0 if z is None else _row_stride(z, "z", None, shape, dev), out.data_ptr(),
-            _row_stride(out, "out", out_dtype, shape, dev), rows, Cd, ngroups, eps, bool(center),
+            _whole(bias, "bias", torch.float32, (Cd,), dev), _ptr(z), zs, out.data_ptr(), os_, rows, Cd, ngroups, eps, bool(center),
             bool(gate_first), _code(y.dtype), SSD_F32 if z is None else _code(z.dtype),
             _code(out_dtype))
     return out
@@ -800,13 +801,13 @@ def group_norm_gate_bwd(dout, y, weight, bias=None, z=None, ngroups=1, eps=1e-5,
     zs = 0 if z is None else _row_stride(z, "z", None, shape, dev)
     wp = _whole(weight, "weight", torch.float32, (Cd,), dev)
     bp = _whole(bias, "bias", torch.float32, (Cd,), dev)
-    g = {"y": _empty(shape, torch.float32, dev),
-         "z": None if z is None else _empty(shape, z.dtype, dev),
-         "weight": _empty((Cd,), torch.float32, dev),
-         "bias": None if bias is None else _empty((Cd,), torch.float32, dev)}
+    g = {"y": y.new_empty(shape, dtype=torch.float32),
+         "z": None if z is None else z.new_empty(shape),
+         "weight": weight.new_empty((Cd,)),
+         "bias": None if bias is None else weight.new_empty((Cd,))}
     if workspace is None:
         need = lib.ssd_group_norm_gate_bwd_workspace_size(rows, Cd, ngroups)
-        workspace = _empty((max(need, 1),), torch.uint8, dev)
+        workspace = y.new_empty((max(need, 1),), dtype=torch.uint8)
     _need(workspace, "workspace", torch.uint8, device=y.device)
     _launch(lib.ssd_group_norm_gate_bwd, dev, dout.data_ptr(), strides[0], y.data_ptr(),
             strides[1], wp, bp, _ptr(z), zs, g["y"].data_ptr(), _ptr(g["z"]),

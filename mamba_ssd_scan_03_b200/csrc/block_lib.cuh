@@ -284,20 +284,35 @@ ssd_status launch_sel_shape(const ssd::cache::SelArgs& k, const SelPlan& p, cuda
   }
 }
 
-template <int LPC>
+template <typename T, typename TD, int LPC>
 ssd_status launch_sel_step(const ssd::cache::SelArgs& k, cudaStream_t stream) {
   namespace cc = ssd::cache;
-  const bool vec = k.dstate % 4 == 0 && aligned16(k.state);
+  // a lane's four states, and four values of B and C, in one access each
+  const size_t four = 4 * sizeof(T);
+  auto in4 = [&](const void* p, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % four == 0 && stride % 4 == 0;
+  };
+  const bool vec = k.dstate % 4 == 0 && aligned16(k.state) && in4(k.B, k.bs) && in4(k.C, k.cs);
   const int64_t dblk = (k.dim + 128 / LPC - 1) / (128 / LPC);
   // four rows per CTA share the rates' loads where that still leaves every SM several CTAs
-  const bool four = dblk * ((k.ntok + 3) / 4) >= 4 * int64_t(sm_count());
-  const dim3 grid(unsigned(four ? (k.ntok + 3) / 4 : k.ntok), unsigned(dblk));
+  const bool four_rows = dblk * ((k.ntok + 3) / 4) >= 4 * int64_t(sm_count());
+  const dim3 grid(unsigned(four_rows ? (k.ntok + 3) / 4 : k.ntok), unsigned(dblk));
   if (dblk > 65535) return SSD_ERR_UNSUPPORTED;
-  if (four && vec) cc::selective_step_kernel<LPC, 4, true><<<grid, 128, 0, stream>>>(k);
-  else if (four) cc::selective_step_kernel<LPC, 4, false><<<grid, 128, 0, stream>>>(k);
-  else if (vec) cc::selective_step_kernel<LPC, 1, true><<<grid, 128, 0, stream>>>(k);
-  else cc::selective_step_kernel<LPC, 1, false><<<grid, 128, 0, stream>>>(k);
+  if (four_rows && vec)
+    cc::selective_step_kernel<T, TD, LPC, 4, true><<<grid, 128, 0, stream>>>(k);
+  else if (four_rows)
+    cc::selective_step_kernel<T, TD, LPC, 4, false><<<grid, 128, 0, stream>>>(k);
+  else if (vec) cc::selective_step_kernel<T, TD, LPC, 1, true><<<grid, 128, 0, stream>>>(k);
+  else cc::selective_step_kernel<T, TD, LPC, 1, false><<<grid, 128, 0, stream>>>(k);
   return launched();
+}
+template <typename T, typename TD>
+ssd_status launch_sel_step_n(const ssd::cache::SelArgs& k, cudaStream_t stream) {
+  if (k.dstate <= 8) return launch_sel_step<T, TD, 2>(k, stream);
+  if (k.dstate <= 16) return launch_sel_step<T, TD, 4>(k, stream);
+  if (k.dstate <= 32) return launch_sel_step<T, TD, 8>(k, stream);
+  if (k.dstate <= 64) return launch_sel_step<T, TD, 16>(k, stream);
+  return launch_sel_step<T, TD, 32>(k, stream);
 }
 
 // ---- group norm --------------------------------------------------------------------------------
@@ -468,12 +483,9 @@ ssd_status ssd_selective_step(const ssd_selective_args* args, int64_t batch,
   if (st != SSD_OK || batch == 0) return st;
   ssd::cache::SelArgs k = sel_args(args);
   k.ntok = batch;
-  const int n = args->dstate;
-  if (n <= 8) return launch_sel_step<2>(k, stream);
-  if (n <= 16) return launch_sel_step<4>(k, stream);
-  if (n <= 32) return launch_sel_step<8>(k, stream);
-  if (n <= 64) return launch_sel_step<16>(k, stream);
-  return launch_sel_step<32>(k, stream);
+  if (!k.io_bf16) return launch_sel_step_n<float, float>(k, stream);
+  if (k.dt_bf16) return launch_sel_step_n<__nv_bfloat16, __nv_bfloat16>(k, stream);
+  return launch_sel_step_n<__nv_bfloat16, float>(k, stream);
 }
 
 ssd_status ssd_group_norm_gate(const void* y, int64_t y_stride, const float* weight,

@@ -64,11 +64,6 @@ __device__ __forceinline__ float softplus_acc(float v) {
   return fmaxf(v, 0.f) + fmaf(w2 * s, p, w2);
 }
 
-__device__ __forceinline__ float load_any(const void* p, int64_t i, bool bf16) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-              : static_cast<const float*>(p)[i];
-}
-
 // NV neighbouring values of a row as they lie in memory (one or two wide accesses), or one value
 // per word.  Loading and converting are kept apart, and nothing branches between a load and the
 // stage that converts it: a value is first waited for there.
@@ -473,66 +468,86 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
 }
 
 // One token of each sequence.  LPC lanes per channel with 4 states each, a warp on 32 / LPC
-// neighbouring channels (one contiguous run of the state), RB rows per CTA so that the rates
-// A are read once for them and RB state loads are in flight.
-template <int LPC, int RB, bool VEC>
+// neighbouring channels (one contiguous run of the state), RB rows per CTA so that the rates A
+// are read once for them and RB rows' loads are in flight: all of a thread's loads are issued
+// before the first is used.  VEC: a lane's four states, and its values of B and C, come in one
+// access each.
+template <typename T, typename TD, int LPC, int RB, bool VEC>
 __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
   const int lane = threadIdx.x & 31;
   const int q = lane % LPC;
   const int d = int(blockIdx.y) * (128 / LPC) + threadIdx.x / LPC;
   const int N = a.dstate, n0 = q * 4;
-  const bool on = d < a.dim;
-  const int g = on ? d / (a.dim / a.ngroups) : 0;
+  const bool on = d < a.dim && n0 < N;
+  const int dc = on ? d : 0;  // lanes off the end read channel 0 and write nothing
+  const int64_t bc = int64_t(dc / (a.dim / a.ngroups)) * N + (on ? n0 : 0);
   const int64_t row0 = int64_t(blockIdx.x) * RB;
   const int64_t batch = a.ntok;
 
-  int64_t slot[RB];
-  float h[RB][4];
+  Raw<T, 4, VEC> rb[RB], rc[RB];
+  Raw<T, 1, false> rx[RB], rz[RB];
+  Raw<TD, 1, false> rd[RB];
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
-    slot[r] = row0 + r < batch ? warp_slot(a.slots, row0 + r, a.nslots) : -1;
-    const float* p = a.state + (slot[r] * a.dim + d) * N + n0;
-    const bool ok = on && slot[r] >= 0;
+    const int64_t row = row0 + r < batch ? row0 + r : batch - 1;
+    rx[r].load1(0, static_cast<const T*>(a.x) + row * a.xs + dc);
+    rd[r].load1(0, static_cast<const TD*>(a.dt) + row * a.dts + dc);
+    if (a.z) rz[r].load1(0, static_cast<const T*>(a.z) + row * a.zs + dc);
+    const T* pb = static_cast<const T*>(a.B) + row * a.bs + bc;
+    const T* pc = static_cast<const T*>(a.C) + row * a.cs + bc;
     if constexpr (VEC) {
-      const float4 v = ok && n0 < N ? *reinterpret_cast<const float4*>(p)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-      h[r][0] = v.x; h[r][1] = v.y; h[r][2] = v.z; h[r][3] = v.w;
+      rb[r].load(pb);
+      rc[r].load(pc);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[r][k] = ok && n0 + k < N ? p[k] : 0.f;
+      for (int k = 0; k < 4; ++k) {
+        rb[r].load1(k, pb + (n0 + k < N ? k : 0));
+        rc[r].load1(k, pc + (n0 + k < N ? k : 0));
+      }
     }
   }
   float av[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    av[k] = on && n0 + k < N ? rate2(a.A[int64_t(d) * N + n0 + k]) : 0.f;
+    av[k] = on && n0 + k < N ? a.A[int64_t(d) * N + n0 + k] : 0.f;
   const float Dd = on && a.D ? a.D[d] : 0.f;
   const float bias = on && a.dt_bias ? a.dt_bias[d] : 0.f;
+  int64_t slot[RB];
+  float h[RB][4];
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    slot[r] = row0 + r < batch ? warp_slot(a.slots, row0 + r, a.nslots) : -1;
+    const float* p = a.state + ((slot[r] < 0 ? 0 : slot[r]) * a.dim + dc) * N + (on ? n0 : 0);
+    if constexpr (VEC) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      h[r][0] = v.x; h[r][1] = v.y; h[r][2] = v.z; h[r][3] = v.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[r][k] = p[n0 + k < N ? k : 0];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) av[k] = rate2(av[k]);
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
     const bool ok = on && slot[r] >= 0;
-    const int64_t row = row0 + r;
-    const float x = ok ? load_any(a.x, row * a.xs + d, a.io_bf16) : 0.f;
-    float dt = ok ? load_any(a.dt, row * a.dts + d, a.dt_bf16) + bias : 0.f;
+    const float x = rx[r].get(0);
+    float dt = rd[r].get(0) + bias;
     if (a.softplus) dt = softplus_acc(dt);
     const float u = dt * x;
     float acc = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const bool in = ok && n0 + k < N;
-      const int64_t at = int64_t(g) * N + n0 + k;
-      const float bv = in ? load_any(a.B, row * a.bs + at, a.io_bf16) : 0.f;
-      const float cv = in ? load_any(a.C, row * a.cs + at, a.io_bf16) : 0.f;
-      h[r][k] = fmaf(ex2(dt * av[k]), h[r][k], u * bv);
-      acc = fmaf(cv, h[r][k], acc);
+      h[r][k] = fmaf(ex2(dt * av[k]), h[r][k], u * rb[r].get(k));
+      if (VEC || n0 + k < N) acc = fmaf(rc[r].get(k), h[r][k], acc);
     }
+    if (!on) acc = 0.f;
 #pragma unroll
     for (int o = 1; o < LPC; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     if (ok) {
       float* p = a.state + (slot[r] * a.dim + d) * N + n0;
       if constexpr (VEC) {
-        if (n0 < N)
-          *reinterpret_cast<float4*>(p) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+        *reinterpret_cast<float4*>(p) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -540,9 +555,10 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
       }
       if (q == 0) {
         float v = fmaf(Dd, x, acc);
-        if (a.z) v *= glue::silu_fast(load_any(a.z, row * a.zs + d, a.io_bf16));
-        if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[row * a.ys + d] = __float2bfloat16_rn(v);
-        else static_cast<float*>(a.y)[row * a.ys + d] = v;
+        if (a.z) v *= glue::silu_fast(rz[r].get(0));
+        const int64_t at = (row0 + r) * a.ys + d;
+        if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+        else static_cast<float*>(a.y)[at] = v;
       }
     }
   }
