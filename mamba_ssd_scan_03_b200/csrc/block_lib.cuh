@@ -208,7 +208,8 @@ ssd_status check_sel(const ssd_selective_args* a, const int32_t* cu, const uint8
       a->nslots > INT32_MAX)
     return SSD_ERR_INVALID_ARG;
   if (!a->state && (a->slots || resume || (!cu && nseq > 0))) return SSD_ERR_INVALID_ARG;
-  if (a->state && !a->slots && a->nslots < nseq) return SSD_ERR_INVALID_ARG;
+  if (a->state && a->nslots < (a->slots ? std::min<int64_t>(nseq, 1) : nseq))
+    return SSD_ERR_INVALID_ARG;
   if (nseq == 0) return SSD_OK;
   const size_t es = dtype_size(a->io);
   const Arg in[] = {rows_arg(a->x, rows, a->x_stride, a->dim, es),

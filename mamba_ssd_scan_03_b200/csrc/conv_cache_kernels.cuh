@@ -114,6 +114,44 @@ __device__ __forceinline__ int64_t warp_slot(const int* __restrict__ slots, int6
   return s;
 }
 
+// The same for RB neighbouring rows from row0 on, in one walk over the earlier slots; rows past
+// `batch` are left alone.  Call with the whole warp.
+template <int RB>
+__device__ __forceinline__ void warp_slots(const int* __restrict__ slots, int64_t row0,
+                                           int64_t batch, int64_t nslots, int (&out)[RB]) {
+  if (!slots) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) out[r] = row0 + r < batch ? int(row0 + r) : -1;
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  unsigned bad = 0;
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    out[r] = row0 + r < batch ? slots[row0 + r] : -1;
+    if (out[r] >= nslots) bad |= 1u << r;
+#pragma unroll
+    for (int e = 0; e < r; ++e)
+      if (out[e] == out[r]) bad |= 1u << r;
+  }
+  for (int64_t j = lane; j < row0; j += 32) {
+    const int s = slots[j];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+      if (s == out[r]) bad |= 1u << r;
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    if (out[r] < 0) {
+      out[r] = -1;
+    } else if (bad >> r & 1u) {
+      out[r] = -1;
+      if (lane == 0) latch_status(SSD_ERR_INDEX, kSiteSlot);
+    }
+  }
+}
+
 // cu_seqlens must not decrease and must stay inside [0, ntok]; a warp latches SSD_ERR_INDEX
 // where it does not.  The kernels clip every access themselves.
 __device__ __forceinline__ void warp_check_seqs(const int* __restrict__ cu, int nseq,
@@ -277,18 +315,18 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs<T> a) {
   const int c0 = int(blockIdx.y * blockDim.x + threadIdx.x) * VW;
   const int64_t row0 = int64_t(blockIdx.x) * RB;
   const bool live = c0 < a.cdim;
-  int64_t slot[RB];
+  int slot[RB];
   float win[RB][K][VW];
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
     const int64_t row = row0 + r < a.ntok ? row0 + r : a.ntok - 1;
     if (live) load_ch<T, VW>(a.u + row * a.us + c0, win[r][K - 1]);
   }
+  warp_slots<RB>(a.slots, row0, a.ntok, a.nslots, slot);
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
-    slot[r] = row0 + r < a.ntok ? warp_slot(a.slots, row0 + r, a.nslots) : -1;
     if (!live || slot[r] < 0) continue;
-    const T* st = a.state + slot[r] * (K - 1) * a.cdim + c0;
+    const T* st = a.state + int64_t(slot[r]) * (K - 1) * a.cdim + c0;
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) load_ch<T, VW>(st + int64_t(k) * a.cdim, win[r][k]);
   }
@@ -302,7 +340,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs<T> a) {
     if (slot[r] < 0) continue;
     float o[VW];
     conv_silu_row<K, VW>(win[r], 0, wr, bv, o);
-    T* st = a.state + slot[r] * (K - 1) * a.cdim + c0;
+    T* st = a.state + int64_t(slot[r]) * (K - 1) * a.cdim + c0;
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) store_ch<T, VW>(st + int64_t(k) * a.cdim, win[r][k + 1]);
     store_ch<T, VW>(a.out + (row0 + r) * a.os + c0, o);

@@ -468,33 +468,40 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
 }
 
 // One token of each sequence.  LPC lanes per channel with 4 states each, a warp on 32 / LPC
-// neighbouring channels (one contiguous run of the state), RB rows per CTA so that the rates A
-// are read once for them and RB rows' loads are in flight: all of a thread's loads are issued
-// before the first is used.  VEC: a lane's four states, and its values of B and C, come in one
-// access each.
+// neighbouring channels (one contiguous run of the state), RB (1 or 4) rows per CTA so that the
+// rates A are read once for them and RB rows' loads are in flight: a thread's loads are issued
+// before the first is used.  With four rows each lane of a channel prepares (softplus) and
+// finishes (gate) a row of its own, and hands dt and dt x to the others by shuffles.  VEC: a
+// lane's four states, and its values of B and C, come in one access each.
 template <typename T, typename TD, int LPC, int RB, bool VEC>
 __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
+  constexpr int OWN = RB == 4 && LPC == 2 ? 2 : 1;  // rows a lane prepares and finishes
   const int lane = threadIdx.x & 31;
   const int q = lane % LPC;
   const int d = int(blockIdx.y) * (128 / LPC) + threadIdx.x / LPC;
   const int N = a.dstate, n0 = q * 4;
   const bool on = d < a.dim && n0 < N;
-  const int dc = on ? d : 0;  // lanes off the end read channel 0 and write nothing
+  const int dc = d < a.dim ? d : 0;  // lanes off the end read channel 0 and write nothing
   const int64_t bc = int64_t(dc / (a.dim / a.ngroups)) * N + (on ? n0 : 0);
   const int64_t row0 = int64_t(blockIdx.x) * RB;
   const int64_t batch = a.ntok;
+  auto own = [&](int i) { return RB == 1 ? 0 : (q & 3) + i * 2; };  // i-th own row
+  auto clamp = [&](int r) { return row0 + r < batch ? row0 + r : batch - 1; };
 
   Raw<T, 4, VEC> rb[RB], rc[RB];
-  Raw<T, 1, false> rx[RB], rz[RB];
-  Raw<TD, 1, false> rd[RB];
+  Raw<T, 1, false> rx[OWN], rz[OWN];
+  Raw<TD, 1, false> rd[OWN];
+#pragma unroll
+  for (int i = 0; i < OWN; ++i) {
+    const int64_t row = clamp(own(i));
+    rx[i].load1(0, static_cast<const T*>(a.x) + row * a.xs + dc);
+    rd[i].load1(0, static_cast<const TD*>(a.dt) + row * a.dts + dc);
+    if (a.z) rz[i].load1(0, static_cast<const T*>(a.z) + row * a.zs + dc);
+  }
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
-    const int64_t row = row0 + r < batch ? row0 + r : batch - 1;
-    rx[r].load1(0, static_cast<const T*>(a.x) + row * a.xs + dc);
-    rd[r].load1(0, static_cast<const TD*>(a.dt) + row * a.dts + dc);
-    if (a.z) rz[r].load1(0, static_cast<const T*>(a.z) + row * a.zs + dc);
-    const T* pb = static_cast<const T*>(a.B) + row * a.bs + bc;
-    const T* pc = static_cast<const T*>(a.C) + row * a.cs + bc;
+    const T* pb = static_cast<const T*>(a.B) + clamp(r) * a.bs + bc;
+    const T* pc = static_cast<const T*>(a.C) + clamp(r) * a.cs + bc;
     if constexpr (VEC) {
       rb[r].load(pb);
       rc[r].load(pc);
@@ -510,14 +517,16 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     av[k] = on && n0 + k < N ? a.A[int64_t(d) * N + n0 + k] : 0.f;
-  const float Dd = on && a.D ? a.D[d] : 0.f;
-  const float bias = on && a.dt_bias ? a.dt_bias[d] : 0.f;
-  int64_t slot[RB];
+  const float Dd = a.D ? a.D[dc] : 0.f;
+  const float bias = a.dt_bias ? a.dt_bias[dc] : 0.f;
+  int slot[RB];
+  warp_slots<RB>(a.slots, row0, batch, a.nslots, slot);
+  float* const at = a.state + int64_t(dc) * N + (on ? n0 : 0);
+  const int64_t per = int64_t(a.dim) * N;
   float h[RB][4];
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
-    slot[r] = row0 + r < batch ? warp_slot(a.slots, row0 + r, a.nslots) : -1;
-    const float* p = a.state + ((slot[r] < 0 ? 0 : slot[r]) * a.dim + dc) * N + (on ? n0 : 0);
+    const float* p = at + (slot[r] < 0 ? 0 : slot[r]) * per;
     if constexpr (VEC) {
       const float4 v = *reinterpret_cast<const float4*>(p);
       h[r][0] = v.x; h[r][1] = v.y; h[r][2] = v.z; h[r][3] = v.w;
@@ -526,26 +535,34 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
       for (int k = 0; k < 4; ++k) h[r][k] = p[n0 + k < N ? k : 0];
     }
   }
+  float dt[OWN], u[OWN], skip[OWN];
+#pragma unroll
+  for (int i = 0; i < OWN; ++i) {
+    const float x = rx[i].get(0);
+    dt[i] = rd[i].get(0) + bias;
+    if (a.softplus) dt[i] = softplus_acc(dt[i]);
+    u[i] = dt[i] * x;
+    skip[i] = Dd * x;
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) av[k] = rate2(av[k]);
+  float acc[RB];
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
-    const bool ok = on && slot[r] >= 0;
-    const float x = rx[r].get(0);
-    float dt = rd[r].get(0) + bias;
-    if (a.softplus) dt = softplus_acc(dt);
-    const float u = dt * x;
-    float acc = 0.f;
+    float dr = dt[0], ur = u[0];
+    if constexpr (RB == 4) {
+      const int from = (lane & ~3) | (LPC == 2 ? (lane & 2) | (r & 1) : r);
+      dr = __shfl_sync(0xffffffffu, dt[LPC == 2 ? r / 2 : 0], from);
+      ur = __shfl_sync(0xffffffffu, u[LPC == 2 ? r / 2 : 0], from);
+    }
+    acc[r] = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      h[r][k] = fmaf(ex2(dt * av[k]), h[r][k], u * rb[r].get(k));
-      if (VEC || n0 + k < N) acc = fmaf(rc[r].get(k), h[r][k], acc);
+      h[r][k] = fmaf(ex2(dr * av[k]), h[r][k], ur * rb[r].get(k));
+      if (on && (VEC || n0 + k < N)) acc[r] = fmaf(rc[r].get(k), h[r][k], acc[r]);
     }
-    if (!on) acc = 0.f;
-#pragma unroll
-    for (int o = 1; o < LPC; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (ok) {
-      float* p = a.state + (slot[r] * a.dim + d) * N + n0;
+    if (on && slot[r] >= 0) {
+      float* p = at + slot[r] * per;
       if constexpr (VEC) {
         *reinterpret_cast<float4*>(p) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
       } else {
@@ -553,14 +570,41 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
         for (int k = 0; k < 4; ++k)
           if (n0 + k < N) p[k] = h[r][k];
       }
-      if (q == 0) {
-        float v = fmaf(Dd, x, acc);
-        if (a.z) v *= glue::silu_fast(rz[r].get(0));
-        const int64_t at = (row0 + r) * a.ys + d;
-        if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-        else static_cast<float*>(a.y)[at] = v;
-      }
     }
+  }
+  // the channel's sums: each lane ends with its own rows'
+  float sum[OWN];
+  if constexpr (RB == 1) {
+    sum[0] = acc[0];
+#pragma unroll
+    for (int o = 1; o < LPC; o <<= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+  } else {
+    const bool b0 = q & 1, b1 = q & 2;
+    const float k0 = (b0 ? acc[1] : acc[0]) +
+                     __shfl_xor_sync(0xffffffffu, b0 ? acc[0] : acc[1], 1);  // row b0
+    const float k1 = (b0 ? acc[3] : acc[2]) +
+                     __shfl_xor_sync(0xffffffffu, b0 ? acc[2] : acc[3], 1);  // row 2 + b0
+    if constexpr (LPC == 2) {
+      sum[0] = k0;
+      sum[1] = k1;
+    } else {
+      sum[0] = (b1 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2);
+#pragma unroll
+      for (int o = 4; o < LPC; o <<= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+    }
+  }
+  if (d >= a.dim || q >= RB) return;
+#pragma unroll
+  for (int i = 0; i < OWN; ++i) {
+    bool ok = false;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) ok |= own(i) == r && slot[r] >= 0;
+    if (!ok) continue;
+    float v = skip[i] + sum[i];
+    if (a.z) v *= glue::silu_fast(rz[i].get(0));
+    const int64_t to = (row0 + own(i)) * a.ys + d;
+    if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
+    else static_cast<float*>(a.y)[to] = v;
   }
 }
 
