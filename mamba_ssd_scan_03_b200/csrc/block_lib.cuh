@@ -346,33 +346,37 @@ NormPlan make_norm_plan(int64_t rows, int cdim, int ngroups, bool wide, int vecs
     p.threads = ((units + p.nv - 1) / p.nv + 31) / 32 * 32;
     p.ok = p.threads <= 1024;
   }
-  p.depth = 1;
-  if (wide) {
-    const size_t row = size_t(p.nv) * vecs * p.threads * 16;
-    p.depth = int(std::max<size_t>(1, std::min<size_t>(ssd::norm::kDepth, kNormSmem / row)));
-    p.smem = p.depth * row;
-    p.ok = p.ok && p.smem <= kNormSmem;
-  }
   const int teams = p.lanes ? p.threads / p.lanes : 1;
   const int gpc = std::min(teams, ngroups), rpc = teams / gpc;
   const int64_t gblk = (ngroups + gpc - 1) / gpc;
-  // CTAs of an SM: about 1024 threads, and what the rings leave of its shared memory
-  const int64_t per_sm = std::max<int64_t>(
-      1, std::min<int64_t>(1024 / p.threads, 200 * 1024 / int64_t(p.smem + 4096)));
-  const int64_t most = std::max<int64_t>(1, sm_count() * per_sm / gblk);
-  p.cta_rows = std::max<int64_t>(1, std::min((rows + rpc - 1) / rpc, most));
+  // CTAs of an SM: about 1024 threads, and what the rings leave of its shared memory.  Rows that one
+  // round of CTAs takes need no ring; else as deep a ring as leaves two CTAs to an SM.
+  const size_t row = wide ? size_t(p.nv) * vecs * p.threads * 16 : 0;
+  auto most = [&](int depth) {
+    const int64_t per_sm = std::max<int64_t>(
+        1, std::min<int64_t>(1024 / p.threads, int64_t(kNormSmem / (depth * row + 4096))));
+    return std::max<int64_t>(1, sm_count() * per_sm / gblk);
+  };
+  p.depth = 1;
+  if (wide && (rows + rpc - 1) / rpc > most(1)) {
+    p.depth = int(std::min<size_t>(ssd::norm::kDepth, std::max<size_t>(2, kNormSmem / 2 / row)));
+    while (p.depth > 1 && p.depth * row > kNormSmem) --p.depth;
+  }
+  p.smem = p.depth * row;
+  p.ok = p.ok && p.smem <= kNormSmem;
+  p.cta_rows = std::max<int64_t>(1, std::min((rows + rpc - 1) / rpc, most(p.depth)));
   p.grid = p.cta_rows * gblk;
   return p;
 }
 
 #define SSD_NORM_VARIANTS(X)                                                                  \
-  X(8, 1, 8, 128) X(32, 1, 8, 128) X(32, 2, 8, 128) X(32, 4, 8, 128) X(0, 1, 8, 256)          \
-  X(0, 2, 8, 512) X(0, 2, 8, 1024) X(32, 1, 1, 128) X(32, 4, 1, 128) X(0, 4, 1, 512)          \
-  X(0, 8, 1, 1024)
+  X(8, 1, 8, 128, 8) X(32, 1, 8, 128, 8) X(32, 2, 8, 128, 4) X(32, 4, 8, 128, 2)              \
+  X(0, 1, 8, 256, 4) X(0, 2, 8, 320, 2) X(0, 2, 8, 512, 1) X(0, 2, 8, 1024, 1)                \
+  X(32, 1, 1, 128, 8) X(32, 4, 1, 128, 8) X(0, 4, 1, 512, 2) X(0, 8, 1, 1024, 1)
 
-// Lets a kernel use the SM's shared memory past 48 KB; once per kernel and device.
+// Lets a kernel use the SM's shared memory past 48 KB; done once per kernel and device.
 bool allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done) {
-  if (bytes <= 48 * 1024) return true;
+  if (bytes <= 12 * 1024) return true;  // with the fixed arrays below 48 KB
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = uint64_t(1) << (dev & 63);
@@ -396,13 +400,17 @@ ssd_status launch_norm_kernel(K kernel, const NormPlan& p, const ssd::norm::Norm
 
 ssd_status launch_norm(const NormPlan& p, const ssd::norm::NormArgs& a, bool bwd,
                        cudaStream_t stream) {
-#define X(L, NV, VW, MAXT)                                                                    \
+#define X(L, NV, VW, MAXT, MINB)                                                              \
   if (p.lanes == L && p.nv == NV && p.vw == VW && p.threads <= MAXT) {                        \
-    static std::atomic<uint64_t> done[2];                                                     \
-    return bwd ? launch_norm_kernel(ssd::norm::group_norm_bwd_kernel<L, NV, VW, MAXT>, p, a,  \
-                                    stream, &done[1])                                         \
-               : launch_norm_kernel(ssd::norm::group_norm_kernel<L, NV, VW, MAXT>, p, a,      \
-                                    stream, &done[0]);                                        \
+    static std::atomic<uint64_t> done[3];                                                     \
+    if (!bwd)                                                                                 \
+      return launch_norm_kernel(ssd::norm::group_norm_kernel<L, NV, VW, MAXT, MINB>, p, a,    \
+                                stream, &done[0]);                                            \
+    if (a.b)                                                                                  \
+      return launch_norm_kernel(ssd::norm::group_norm_bwd_kernel<L, NV, VW, MAXT, MINB, true>, \
+                                p, a, stream, &done[1]);                                      \
+    return launch_norm_kernel(ssd::norm::group_norm_bwd_kernel<L, NV, VW, MAXT, MINB, false>, \
+                              p, a, stream, &done[2]);                                        \
   }
   SSD_NORM_VARIANTS(X)
 #undef X

@@ -22,6 +22,9 @@
 namespace ssd {
 namespace norm {
 
+using cache::dup;
+using cache::sigmoid2;
+
 struct NormArgs {
   const void* y;
   const void* z;
@@ -127,8 +130,6 @@ struct Place {
   __device__ __forceinline__ int col(int i) const { return (i * lanes + lane) * VW; }
 };
 
-__device__ __forceinline__ float sigm(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-
 // A thread's inputs of its next rows.  VW = 8: a ring of kDepth rows in shared memory that the
 // thread fills for itself with 16-byte asynchronous copies, so that the loads of later rows are in
 // flight while a row is worked on, and no barrier is needed.  VW = 1: plain loads.
@@ -162,42 +163,58 @@ __device__ __forceinline__ void norm_fill(const NormArgs& a, const Place<LANES, 
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
 }
-// y, z and dout of unit i of the row that the ring's oldest stage holds (zeros off the end).
+// One input of a row: where a thread finds its 16-byte pieces in the ring, or in memory.
+struct Stream {
+  const void* p;
+  int64_t stride;
+  int first;  // piece of a unit
+  bool bf16;
+};
 template <int LANES, int NV, int VW>
-__device__ __forceinline__ void norm_take(const NormArgs& a, const Place<LANES, NV, VW>& p, int c0,
-                                          int64_t row, const uint4* ring, int i, float (&y)[VW],
-                                          float (&z)[VW], float (&d)[VW]) {
-  const int c = p.col(i);
-  const bool in = p.on && row < a.rows && c < p.gs;
-#pragma unroll
-  for (int j = 0; j < VW; ++j) y[j] = z[j] = d[j] = 0.f;
-  if (!in) return;
+struct Streams {
+  Stream y, z, d;
+  int per;  // pieces of a unit
+  __device__ __forceinline__ explicit Streams(const NormArgs& a) {
+    y = {a.y, a.ys, 0, a.y_bf16};
+    z = {a.z, a.zs, y.bf16 ? 1 : 2, a.z_bf16};
+    d = {a.dout, a.os, z.first + (a.z ? (a.z_bf16 ? 1 : 2) : 0), a.o_bf16};
+    per = ring_vecs(a);
+  }
+};
+// The VW values of unit i, which holds channel c0 + col(i), of the row whose stage `ring` is; the
+// caller has checked that the unit lies in the group and the row among the rows.
+template <int VW>
+__device__ __forceinline__ void norm_take(const Stream& s, int per, const uint4* ring, int i,
+                                          int64_t row, int c, float (&v)[VW]) {
   if constexpr (VW == 8) {
-    const uint4* from = ring + i * ring_vecs(a) * blockDim.x;
-    auto take = [&](float (&v)[VW], bool bf16) {
-      const uint4 u = *from;
-      from += blockDim.x;
-      if (bf16) {
-        v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
-        v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
-      } else {
-        const uint4 t = *from;
-        from += blockDim.x;
-        v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
-        v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
-        v[4] = __uint_as_float(t.x); v[5] = __uint_as_float(t.y);
-        v[6] = __uint_as_float(t.z); v[7] = __uint_as_float(t.w);
-      }
-    };
-    take(y, a.y_bf16);
-    if (a.z) take(z, a.z_bf16);
-    if (a.dout) take(d, a.o_bf16);
+    const uint4* from = ring + (i * per + s.first) * int(blockDim.x);
+    const uint4 u = from[0];
+    if (s.bf16) {
+      v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
+      v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
+    } else {
+      const uint4 t = from[blockDim.x];
+      v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+      v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+      v[4] = __uint_as_float(t.x); v[5] = __uint_as_float(t.y);
+      v[6] = __uint_as_float(t.z); v[7] = __uint_as_float(t.w);
+    }
   } else {
-    load_n<VW>(a.y, row * a.ys + c0 + c, a.y_bf16, y);
-    if (a.z) load_n<VW>(a.z, row * a.zs + c0 + c, a.z_bf16, z);
-    if (a.dout) load_n<VW>(a.dout, row * a.os + c0 + c, a.o_bf16, d);
+    load_n<VW>(s.p, row * s.stride + c, s.bf16, v);
   }
 }
+// Pairs of values (VW = 1: one value and a zero).
+template <int VW>
+__device__ __forceinline__ float2 pair(const float (&v)[VW], int j) {
+  if constexpr (VW == 1) return make_float2(v[0], 0.f);
+  else return make_float2(v[j], v[j + 1]);
+}
+template <int VW>
+__device__ __forceinline__ void put(float (&v)[VW], int j, float2 f) {
+  v[j] = f.x;
+  if constexpr (VW > 1) v[j + 1] = f.y;
+}
+
 // The rows of a CTA: row(k) is handed on with its ring stage when its copies have landed.
 template <int LANES, int NV, int VW, typename F>
 __device__ __forceinline__ void norm_rows(const NormArgs& a, const Place<LANES, NV, VW>& p, int c0,
@@ -223,61 +240,88 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, const Place<LANES, 
   if constexpr (VW == 8) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Threads of a CTA: 128 in teams of lanes, at most MAXT as one team (which bounds the registers).
-template <int LANES, int NV, int VW, int MAXT>
-__global__ void __launch_bounds__(MAXT) group_norm_kernel(const NormArgs a) {
+// Threads of a CTA: 128 in teams of lanes, at most MAXT as one team; MINB CTAs to an SM (the two
+// bound the registers).
+template <int LANES, int NV, int VW, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) group_norm_kernel(const NormArgs a) {
+  constexpr int STEP = VW == 1 ? 1 : 2;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float buf[2][2][1][32];
   const Place<LANES, NV, VW> p(a);
+  const Streams<LANES, NV, VW> in(a);
   const int c0 = p.group * p.gs;
   const float inv = 1.f / p.gs;
-  float w[NV][VW], bb[NV][VW];
+  const bool first = a.z && a.gate_first, last = a.z && !a.gate_first;
+  float w[NV][VW];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VW; ++j) {
-      const int c = p.col(i) + j;
-      const bool in = p.on && c < p.gs;
-      w[i][j] = in ? __ldg(a.w + c0 + c) : 0.f;
-      bb[i][j] = in && a.b ? __ldg(a.b + c0 + c) : 0.f;
-    }
+    if (p.on && p.col(i) < p.gs) load_n<VW>(a.w, c0 + p.col(i), false, w[i]);
   norm_rows(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
     const bool live = p.on && row < a.rows;
-    float v[NV][VW], zv[NV][VW], none[VW];
-    float s[1] = {0.f};
+    float v[NV][VW];
+    float2 s2 = dup(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      norm_take(a, p, c0, row, st, i, v[i], zv[i], none);
+      const int c = p.col(i);
+      if (live && c < p.gs) {
+        norm_take<VW>(in.y, in.per, st, i, row, c0 + c, v[i]);
+        if (first) {
+          float z[VW];
+          norm_take<VW>(in.z, in.per, st, i, row, c0 + c, z);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        if (a.z && a.gate_first) v[i][j] *= glue::silu_fast(zv[i][j]);
-        s[0] += v[i][j];
+          for (int j = 0; j < VW; j += STEP) {
+            const float2 zz = pair<VW>(z, j);
+            put<VW>(v[i], j, mul2(pair<VW>(v[i], j), mul2(zz, sigmoid2(zz))));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) v[i][j] = 0.f;
       }
     }
-    float mu = 0.f;
     if (a.center) {
+      float s[1];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VW; j += STEP) s2 = cache::add2(s2, pair<VW>(v[i], j));
+      s[0] = s2.x + s2.y;
       team_sum<LANES>(s, buf[par][0]);
-      mu = s[0] * inv;
+      const float mu = s[0] * inv;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (p.col(i) < p.gs)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) v[i][j] -= mu;
+      s2 = dup(0.f);
     }
-    s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        v[i][j] -= p.col(i) < p.gs ? mu : 0.f;
-        s[0] = fmaf(v[i][j], v[i][j], s[0]);
-      }
+      for (int j = 0; j < VW; j += STEP) s2 = fma2(pair<VW>(v[i], j), pair<VW>(v[i], j), s2);
+    float s[1] = {s2.x + s2.y};
     team_sum<LANES>(s, buf[par][1]);
-    const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
+    const float2 rstd = dup(rsqrtf(fmaf(s[0], inv, a.eps)));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = p.col(i);
       if (live && c < p.gs) {
         float o[VW];
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          o[j] = fmaf(v[i][j] * rstd, w[i][j], bb[i][j]);
-          if (a.z && !a.gate_first) o[j] *= glue::silu_fast(zv[i][j]);
+        for (int j = 0; j < VW; j += STEP)
+          put<VW>(o, j, mul2(mul2(pair<VW>(v[i], j), rstd), pair<VW>(w[i], j)));
+        if (a.b) {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) o[j] += __ldg(a.b + c0 + c + j);
+        }
+        if (last) {
+          float z[VW];
+          norm_take<VW>(in.z, in.per, st, i, row, c0 + c, z);
+#pragma unroll
+          for (int j = 0; j < VW; j += STEP) {
+            const float2 zz = pair<VW>(z, j);
+            put<VW>(o, j, mul2(pair<VW>(o, j), mul2(zz, sigmoid2(zz))));
+          }
         }
         store_n<VW>(a.out, row * a.os + c0 + c, a.o_bf16, o);
       }
@@ -285,73 +329,109 @@ __global__ void __launch_bounds__(MAXT) group_norm_kernel(const NormArgs a) {
   });
 }
 
-template <int LANES, int NV, int VW, int MAXT>
-__global__ void __launch_bounds__(MAXT) group_norm_bwd_kernel(const NormArgs a) {
+// BIAS: sums db as well.  The row's values are read from the ring again for the gradients rather
+// than held in registers across the sums.
+template <int LANES, int NV, int VW, int MAXT, int MINB, bool BIAS>
+__global__ void __launch_bounds__(MAXT, MINB) group_norm_bwd_kernel(const NormArgs a) {
+  constexpr int STEP = VW == 1 ? 1 : 2;
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float buf[2][2][3][32];
   Place<LANES, NV, VW> p(a);
+  const Streams<LANES, NV, VW> in(a);
   const int c0 = p.group * p.gs;
-  float w[NV][VW], dw[NV][VW], db[NV][VW];
+  float w[NV][VW], dw[NV][VW], db[BIAS ? NV : 1][VW];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    if (p.on && p.col(i) < p.gs) load_n<VW>(a.w, c0 + p.col(i), false, w[i]);
 #pragma unroll
     for (int j = 0; j < VW; ++j) {
-      const int c = p.col(i) + j;
-      w[i][j] = p.on && c < p.gs ? __ldg(a.w + c0 + c) : 0.f;
-      dw[i][j] = db[i][j] = 0.f;
+      dw[i][j] = 0.f;
+      if (BIAS) db[i][j] = 0.f;
     }
+  }
   const float inv = 1.f / p.gs;
-  const bool first = a.z && a.gate_first, gate_last = a.z && !a.gate_first;
+  const bool first = a.z && a.gate_first, last = a.z && !a.gate_first;
   norm_rows(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
     const bool live = p.on && row < a.rows;
-    float y[NV][VW], z[NV][VW], d[NV][VW];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) norm_take(a, p, c0, row, st, i, y[i], z[i], d[i]);
+    // v and do of a unit's pair j, as both passes need them
+    float y[VW], z[VW], d[VW];
+    auto take = [&](int i) {
+      const int c = c0 + p.col(i);
+      norm_take<VW>(in.y, in.per, st, i, row, c, y);
+      norm_take<VW>(in.d, in.per, st, i, row, c, d);
+      if (a.z) norm_take<VW>(in.z, in.per, st, i, row, c, z);
+    };
     float mu = 0.f;
     if (a.center) {
       float s[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < NV; ++i)
+        if (live && p.col(i) < p.gs) {
+          take(i);
 #pragma unroll
-        for (int j = 0; j < VW; ++j)
-          s[0] += first ? y[i][j] * glue::silu_fast(z[i][j]) : y[i][j];
+          for (int j = 0; j < VW; ++j) s[0] += first ? y[j] * cache::silu(z[j]) : y[j];
+        }
       team_sum<LANES>(s, buf[par][0]);
       mu = s[0] * inv;
     }
     // sums of (v - mu)^2, dn (v - mu) and dn
-    float s[3] = {0.f, 0.f, 0.f};
+    float2 t0 = dup(0.f), t1 = dup(0.f), t2 = dup(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
+      if (live && p.col(i) < p.gs) {
+        take(i);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        const float sg = a.z ? sigm(z[i][j]) : 0.f;
-        const float v = (first ? y[i][j] * (z[i][j] * sg) : y[i][j]) -
-                        (p.col(i) < p.gs ? mu : 0.f);
-        const float dn = (gate_last ? d[i][j] * (z[i][j] * sg) : d[i][j]) * w[i][j];
-        s[0] = fmaf(v, v, s[0]);
-        s[1] = fmaf(dn, v, s[1]);
-        s[2] += dn;
+        for (int j = 0; j < VW; j += STEP) {
+          float2 v = pair<VW>(y, j), dn = pair<VW>(d, j);
+          if (a.z) {
+            const float2 zz = pair<VW>(z, j), g = mul2(zz, sigmoid2(zz));
+            if (first) v = mul2(v, g);
+            else dn = mul2(dn, g);
+          }
+          v = cache::add2(v, make_float2(-mu, VW == 1 ? 0.f : -mu));
+          dn = mul2(dn, pair<VW>(w[i], j));
+          t0 = fma2(v, v, t0);
+          t1 = fma2(dn, v, t1);
+          t2 = cache::add2(t2, dn);
+        }
       }
+    float s[3] = {t0.x + t0.y, t1.x + t1.y, t2.x + t2.y};
     team_sum<LANES>(s, buf[par][1]);
     const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
-    const float c1 = s[1] * rstd * inv, c2 = a.center ? s[2] * inv : 0.f;
+    const float2 r2 = dup(rstd), c1 = dup(-s[1] * rstd * inv);
+    const float2 c2 = dup(a.center ? -s[2] * inv : 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = p.col(i);
       if (live && c < p.gs) {
+        take(i);
         float ody[VW], odz[VW];
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          const float zj = z[i][j], sg = a.z ? sigm(zj) : 0.f;
-          const float silu = zj * sg, slope = sg * (1.f + zj * (1.f - sg));
-          const float n = ((first ? y[i][j] * silu : y[i][j]) - mu) * rstd;
-          const float doj = gate_last ? d[i][j] * silu : d[i][j];
-          dw[i][j] = fmaf(doj, n, dw[i][j]);
-          db[i][j] += doj;
-          const float dv = rstd * (doj * w[i][j] - c2 - n * c1);
-          ody[j] = first ? dv * silu : dv;
-          odz[j] = first ? dv * y[i][j] * slope
-                         : d[i][j] * fmaf(n, w[i][j], a.b ? a.b[c0 + c + j] : 0.f) * slope;
+        for (int j = 0; j < VW; j += STEP) {
+          const float2 yy = pair<VW>(y, j), ww = pair<VW>(w[i], j);
+          float2 v = yy, dd = pair<VW>(d, j), g = dup(1.f), slope = dup(0.f);
+          if (a.z) {
+            const float2 zz = pair<VW>(z, j), sg = sigmoid2(zz);
+            g = mul2(zz, sg);
+            // silu' = sg (1 + z (1 - sg)) = sg + g - g sg
+            slope = fma2(make_float2(-g.x, -g.y), sg, cache::add2(sg, g));
+            if (first) v = mul2(yy, g);
+          }
+          const float2 n = mul2(cache::add2(v, dup(-mu)), r2);
+          if (last) {
+            float2 o = mul2(n, ww);
+            if (BIAS) {
+              o.x += __ldg(a.b + c0 + c + j);
+              if (VW > 1) o.y += __ldg(a.b + c0 + c + j + 1);
+            }
+            put<VW>(odz, j, mul2(mul2(dd, o), slope));
+            dd = mul2(dd, g);
+          }
+          put<VW>(dw[i], j, fma2(dd, n, pair<VW>(dw[i], j)));
+          if (BIAS) put<VW>(db[i], j, cache::add2(pair<VW>(db[i], j), dd));
+          const float2 dv = mul2(r2, fma2(dd, ww, fma2(n, c1, c2)));
+          put<VW>(ody, j, first ? mul2(dv, g) : dv);
+          if (first) put<VW>(odz, j, mul2(mul2(dv, yy), slope));
         }
         store_n<VW>(a.dy, row * int64_t(a.cdim) + c0 + c, false, ody);
         if (a.z) store_n<VW>(a.dz, row * int64_t(a.cdim) + c0 + c, a.z_bf16, odz);
@@ -359,11 +439,11 @@ __global__ void __launch_bounds__(MAXT) group_norm_bwd_kernel(const NormArgs a) 
     }
   });
   // one row of partial sums per CTA; the teams of one group add theirs in turn
-  const int per = a.b ? 2 : 1;
+  constexpr int per = BIAS ? 2 : 1;
   float* to = a.part + int64_t(p.cta_row) * per * a.cdim + c0;
   if constexpr (LANES != 0) {
     constexpr int kCols = MAXT * NV * VW;
-    __shared__ float acc[2][kCols];
+    __shared__ float acc[per][kCols];
     const int base = (p.team % p.gpc) * p.gs;
     for (int k = 0; k < p.rpc; ++k) {
       if (p.on && p.sub == k) {
@@ -375,10 +455,10 @@ __global__ void __launch_bounds__(MAXT) group_norm_bwd_kernel(const NormArgs a) 
             if (c < p.gs) {
               if (k > 0) {
                 dw[i][j] += acc[0][base + c];
-                db[i][j] += acc[1][base + c];
+                if constexpr (BIAS) db[i][j] += acc[1][base + c];
               }
               acc[0][base + c] = dw[i][j];
-              acc[1][base + c] = db[i][j];
+              if constexpr (BIAS) acc[1][base + c] = db[i][j];
             }
           }
       }
@@ -392,7 +472,7 @@ __global__ void __launch_bounds__(MAXT) group_norm_bwd_kernel(const NormArgs a) 
       const int c = p.col(i);
       if (c < p.gs) {
         store_n<VW>(to, c, false, dw[i]);
-        if (a.b) store_n<VW>(to + a.cdim, c, false, db[i]);
+        if constexpr (BIAS) store_n<VW>(to + a.cdim, c, false, db[i]);
       }
     }
   }

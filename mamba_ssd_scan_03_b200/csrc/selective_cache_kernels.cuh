@@ -54,7 +54,7 @@ __device__ __forceinline__ float rate2(float a) {
 // by the odd series w + w^3/3 + w^5/5 + ...; the terms past w^13 / 13 are below 2^-25 of it.
 __device__ __forceinline__ float softplus_acc(float v) {
   const float e = ex2(-fabsf(v) * kLog2e);
-  const float w = __fdividef(e, 2.f + e), s = w * w;
+  const float w = e * rcp(2.f + e), s = w * w;
   float p = fmaf(s, 1.f / 13.f, 1.f / 11.f);
   p = fmaf(s, p, 1.f / 9.f);
   p = fmaf(s, p, 1.f / 7.f);
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
         const float4 f = *reinterpret_cast<const float4*>(pp);
         v[i] = skip[i] + ((f.x + f.y) + (f.z + f.w));
       }
-      if (pz) v[i] *= glue::silu_fast(zc.get(i));
+      if (pz) v[i] *= silu(zc.get(i));
     }
     if constexpr (VEC) {
       if (eon && t + row(0) < t1) {
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
     for (int r = 0; r < RB; ++r) ok |= own(i) == r && slot[r] >= 0;
     if (!ok) continue;
     float v = skip[i] + sum[i];
-    if (a.z) v *= glue::silu_fast(rz[i].get(0));
+    if (a.z) v *= silu(rz[i].get(0));
     const int64_t to = (row0 + own(i)) * a.ys + d;
     if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
     else static_cast<float*>(a.y)[to] = v;
