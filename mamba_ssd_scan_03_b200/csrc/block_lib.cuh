@@ -153,29 +153,24 @@ ssd_status run_conv(const void* u, int64_t us, const float* w, const float* bias
 
 // ---- selective scan ----------------------------------------------------------------------------
 
-// How packed prompts are scanned: channels per warp, and tokens per chunk (0: whole sequences).
+// How packed prompts are scanned: lanes per channel, and tokens per chunk (0: whole sequences).
 struct SelPlan {
-  int lpc;  // lanes per channel
-  int r;    // channels per lane
+  int lpc;
   int chunk;
   int64_t units;
 };
-int sel_channels(int lpc, int r) { return 32 / lpc * r; }
+int64_t sel_blocks(int dim, int ngroups, int lpc) {  // warps per unit
+  const int dpg = dim / ngroups, ch = 32 / lpc;
+  return int64_t(ngroups) * ((dpg + ch - 1) / ch);
+}
 
 SelPlan make_sel_plan(int64_t ntok, int nseq, int dim, int dstate, int ngroups, int64_t maxlen) {
   SelPlan p;
   p.lpc = 2;
-  while (p.lpc * 4 < dstate) p.lpc *= 2;
-  p.r = p.lpc <= 4 ? 1 : p.lpc / 4;
-  const int dpg = dim / ngroups;
-  auto blocks = [&](int r) {
-    const int ch = sel_channels(p.lpc, r);
-    return int64_t(ngroups) * ((dpg + ch - 1) / ch);
-  };
+  while (p.lpc * 8 < dstate) p.lpc *= 2;
   const int64_t sched = 4 * int64_t(sm_count());  // warp schedulers
-  (void)0;
   const int64_t len = std::min(ntok, maxlen > 0 ? maxlen : (ntok + nseq - 1) / nseq);
-  const int64_t warps = nseq * blocks(p.r);
+  const int64_t warps = nseq * sel_blocks(dim, ngroups, p.lpc);
   p.chunk = 0;
   p.units = nseq;
   if (warps < sched && len >= 128) {
@@ -242,19 +237,18 @@ ssd::cache::SelArgs sel_args(const ssd_selective_args* a) {
   return k;
 }
 
-template <typename T, typename TD, int LPC, int R, bool VEC>
+template <typename T, typename TD, int LPC, int SPL, bool VEC>
 ssd_status launch_sel(const ssd::cache::SelArgs& k, const SelPlan& p, cudaStream_t stream) {
   namespace cc = ssd::cache;
-  const int dpg = k.dim / k.ngroups, ch = sel_channels(LPC, R);
-  const int64_t ncb = int64_t(k.ngroups) * ((dpg + ch - 1) / ch);
+  const int64_t ncb = sel_blocks(k.dim, k.ngroups, LPC);
   if (p.units * ncb > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   const unsigned grid = unsigned(p.units * ncb);
   if (k.chunk) {
-    cc::selective_varlen_kernel<T, TD, LPC, R, VEC, true><<<grid, 32, 0, stream>>>(k);
+    cc::selective_varlen_kernel<T, TD, LPC, SPL, VEC, true><<<grid, 32, 0, stream>>>(k);
     const ssd_status st = launched();
     if (st != SSD_OK) return st;
   }
-  cc::selective_varlen_kernel<T, TD, LPC, R, VEC, false><<<grid, 32, 0, stream>>>(k);
+  cc::selective_varlen_kernel<T, TD, LPC, SPL, VEC, false><<<grid, 32, 0, stream>>>(k);
   return launched();
 }
 // Wide loads take whole rows of 8 or 16 states and channel groups that start and end on a lane's
@@ -265,23 +259,19 @@ bool sel_wide(const ssd::cache::SelArgs& k) {
          rows16(k.x, k.xs, es) && rows16(k.dt, k.dts, ed) && rows16(k.B, k.bs, es) &&
          rows16(k.C, k.cs, es) && (!k.z || rows16(k.z, k.zs, es)) && rows16(k.y, k.ys, ey);
 }
-
 template <typename T, typename TD>
 ssd_status launch_sel_shape(const ssd::cache::SelArgs& k, const SelPlan& p, cudaStream_t stream) {
   const bool wide = sel_wide(k);
+  if (k.dstate <= 8)
+    return wide ? launch_sel<T, TD, 2, 4, true>(k, p, stream)
+                : launch_sel<T, TD, 2, 4, false>(k, p, stream);
   switch (p.lpc) {
     case 2:
-      return wide ? launch_sel<T, TD, 2, 1, true>(k, p, stream)
-                  : launch_sel<T, TD, 2, 1, false>(k, p, stream);
-    case 4:
-      if (p.r == 2)
-        return wide ? launch_sel<T, TD, 4, 2, true>(k, p, stream)
-                    : launch_sel<T, TD, 4, 2, false>(k, p, stream);
-      return wide ? launch_sel<T, TD, 4, 1, true>(k, p, stream)
-                  : launch_sel<T, TD, 4, 1, false>(k, p, stream);
-    case 8: return launch_sel<T, TD, 8, 2, false>(k, p, stream);
-    case 16: return launch_sel<T, TD, 16, 4, false>(k, p, stream);
-    default: return launch_sel<T, TD, 32, 8, false>(k, p, stream);
+      return wide ? launch_sel<T, TD, 2, 8, true>(k, p, stream)
+                  : launch_sel<T, TD, 2, 8, false>(k, p, stream);
+    case 4: return launch_sel<T, TD, 4, 8, false>(k, p, stream);
+    case 8: return launch_sel<T, TD, 8, 8, false>(k, p, stream);
+    default: return launch_sel<T, TD, 16, 8, false>(k, p, stream);
   }
 }
 

@@ -64,6 +64,20 @@ __device__ __forceinline__ float softplus_acc(float v) {
   return fmaxf(v, 0.f) + fmaf(w2 * s, p, w2);
 }
 
+// The same of a pair.
+__device__ __forceinline__ float2 softplus_acc2(float2 v) {
+  const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
+  const float2 b = add2(e, dup(2.f));
+  const float2 w = mul2(e, make_float2(rcp(b.x), rcp(b.y))), s = mul2(w, w);
+  float2 p = fma2(s, dup(1.f / 13.f), dup(1.f / 11.f));
+  p = fma2(s, p, dup(1.f / 9.f));
+  p = fma2(s, p, dup(1.f / 7.f));
+  p = fma2(s, p, dup(1.f / 5.f));
+  p = fma2(s, p, dup(1.f / 3.f));
+  const float2 w2 = add2(w, w);
+  return add2(make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)), fma2(mul2(w2, s), p, w2));
+}
+
 // NV neighbouring values of a row as they lie in memory (one or two wide accesses), or one value
 // per word.  Loading and converting are kept apart, and nothing branches between a load and the
 // stage that converts it: a value is first waited for there.
@@ -95,44 +109,41 @@ struct Raw {
   }
 };
 
-// LPC lanes per channel, each holding 4 of its (up to 4 LPC) states; R channels per lane.
-template <int LPC, int R>
-struct SelShape {
-  static constexpr int kCg = 32 / LPC;         // channel sets of a warp
-  static constexpr int kCh = kCg * R;          // channels of a warp
-  static constexpr int kNp = LPC * 4;          // states, padded
-  static constexpr int kTok = LPC <= 4 ? 16 : 8;  // tokens staged together
-  static constexpr int kDu = 2 * kCh;          // floats per staged row of (dt, dt x) pairs
-  static constexpr int kPp = LPC < 4 ? LPC : 4;  // partial sums of y per channel
-  static constexpr int kY = kPp * kCh;         // floats per row of them
-  static constexpr int kEx = kTok * kCh / 32;  // x, dt, z elements per lane and stage
-  static constexpr int kEb = kTok * kNp / 32;  // B, C elements per lane and stage
-  static_assert(kTok * kCh % 32 == 0 && 32 % kCh == 0, "whole rows per step of the warp");
-  // Place of channel c's partial sums in the row of token t, in floats.  The four-way exchange
-  // with t puts what the lanes of a quarter warp read together (the same channels of four
-  // rows) on banks of their own.
-  static __device__ __forceinline__ int part(int t, int c) {
-    if constexpr (LPC == 2) return ((c >> 1) ^ (t & 3)) * 4 + (c & 1) * 2;
-    else return (c ^ (t & 3)) * 4;
-  }
-};
-
-// One warp scans one unit: a sequence (chunk == 0) or a chunk of one, for kCh channels of one
-// group.  SUMMARY: only the state after the chunk, from zero (or, for a sequence's first chunk,
-// from the sequence's initial state), and the chunk's sum of dt; those give the scan of a later
-// chunk its entering state, h <- exp(A sum_dt) h + S chunk by chunk.
+// One warp scans one unit: a sequence (chunk == 0) or a chunk of one, for 32 / LPC channels of
+// one group; LPC lanes per channel hold SPL of its states each.  SUMMARY: only the state after
+// the chunk, from zero (or, for a sequence's first chunk, from the sequence's initial state), and
+// the chunk's sum of dt; those give the scan of a later chunk its entering state,
+// h <- exp(A sum_dt) h + S chunk by chunk.
 //
-// Inputs come in stages of kTok tokens: the next stage's loads are issued into registers ahead
-// of the current stage's steps, then converted (softplus, dt x, D x) once per element into
-// shared memory, where the lanes of a channel all read them.  VEC: a lane loads kEx neighbouring
-// channels of one row (and kEb neighbouring states) in one access, which asks for rows of 16-byte
-// multiples; else neighbouring lanes load neighbouring channels one by one.
-template <typename T, typename TD, int LPC, int R, bool VEC, bool SUMMARY>
+// Tokens come in stages of 16: the next stage's values are loaded into registers ahead of the
+// current stage's steps, then converted (softplus, dt x, D x) once per element into shared memory,
+// where the lanes of a channel read them.  VEC: a lane loads EX neighbouring channels of one row
+// (and EB neighbouring states) in one access, which asks for rows of 16-byte multiples; else
+// neighbouring lanes load neighbouring channels one by one.  Nothing branches between a load and
+// its use, and addresses are a pointer per input that moves on by a stage: with one or two warps
+// to a scheduler every instruction outside the steps is time of its own.
+// Why two lanes per channel for 16 states: reading B and C fills registers at 128 bytes a clock
+// and SM, or 256 where a warp reads one or two addresses, and every lane reads its states' B and
+// C anew; with four lanes of four states that takes longer than the exponentials.
+constexpr int kStage = 16;
+
+template <typename T, typename TD, int LPC, int SPL, bool VEC, bool SUMMARY>
 __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
-  using S = SelShape<LPC, R>;
-  constexpr int TK = S::kTok, CH = S::kCh, NP = S::kNp, EX = S::kEx, EB = S::kEb;
-  // arrays of their own, so that the compiler may move a token's loads over the stores before it
-  __shared__ __align__(16) float du[TK * S::kDu], bsm[TK * NP], csm[TK * NP], ysm[TK * S::kY];
+  constexpr int CH = 32 / LPC;         // channels of a warp
+  constexpr int NP = LPC * SPL;        // states, padded
+  constexpr int EX = CH / 2;           // x, dt, z elements per lane and stage
+  constexpr int EB = NP / 2;           // B, C elements per lane and stage
+  constexpr int P = SPL / 2;           // pairs of states
+  constexpr int RX = VEC ? 0 : 32 / CH;  // rows between a lane's elements
+  constexpr int RB = VEC ? 0 : (NP >= 32 ? 1 : 32 / NP);
+  constexpr int CB = NP / 32 > 1 ? NP / 32 : 1;  // B, C elements of a row per lane
+  // arrays of their own, so that the compiler may move loads of one over stores to another
+  __shared__ __align__(16) float2 du[kStage * CH];
+  __shared__ __align__(16) float bsm[kStage * NP], csm[SUMMARY ? 4 : kStage * NP];
+  __shared__ __align__(16) float ysm[SUMMARY ? 4 : kStage * 32];
+  // place of channel c in the rows of token k: what lanes on the same channels of eight rows touch
+  // together lies on banks of its own
+  auto place = [](int k, int c) { return c ^ (k & (CH < 8 ? CH - 1 : 7)); };
 
   const int lane = threadIdx.x;
   const int dpg = a.dim / a.ngroups;
@@ -184,287 +195,251 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
   const bool last = chunk == nchunk - 1;
   const bool resume = a.state && a.resume && a.resume[seq];
 
-  // this lane's channels, states and constants
-  const int q = lane % LPC, cg = lane / LPC;
-  float2 a01[R], a23[R], h01[R], h23[R];
-  float sdt[R];
+  // this lane's channel, states and constants
+  const int q = lane % LPC, ch = lane / LPC;
+  const bool con = ch < nch;
+  const int d = d0 + (con ? ch : 0);
+  float2 av[P], h[P];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int c = cg * R + r;
-    float av[4], hv[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = q * 4 + k;
-      const bool on = c < nch && n < N;
-      av[k] = on ? rate2(a.A[int64_t(d0 + c) * N + n]) : 0.f;
-      hv[k] = on && resume && chunk == 0 && (SUMMARY || nchunk == 1)
-                  ? a.state[(slot * a.dim + d0 + c) * N + n] : 0.f;
-      if (on && !SUMMARY && nchunk > 1) {
-        // a sequence cut into chunks: its initial state was copied by the summary launch (the
-        // last chunk may already have moved the slot's), the others' follow from the summaries
-        const int64_t u0 = unit - chunk;
-        if (chunk == 0) {
-          if (resume) hv[k] = a.ws_state[((u0 + nchunk - 1) * a.dim + d0 + c) * N + n];
-        } else {
-          float h = a.ws_state[(u0 * a.dim + d0 + c) * N + n];
-          for (int j = 1; j < chunk; ++j)
-            h = fmaf(ex2(av[k] * a.ws_dt[(u0 + j) * a.dim + d0 + c]), h,
-                     a.ws_state[((u0 + j) * a.dim + d0 + c) * N + n]);
-          hv[k] = h;
-        }
+  for (int k = 0; k < SPL; ++k) {
+    const int n = q * SPL + k;
+    const bool on = con && n < N;
+    const float rate = on ? rate2(a.A[int64_t(d) * N + n]) : 0.f;
+    float hv = 0.f;
+    if (on && resume && chunk == 0 && (SUMMARY || nchunk == 1))
+      hv = a.state[(slot * a.dim + d) * N + n];
+    if (on && !SUMMARY && nchunk > 1) {
+      // a sequence cut into chunks: its initial state was copied by the summary launch (the last
+      // chunk may already have moved the slot's), the others' follow from the summaries
+      const int64_t u0 = unit - chunk;
+      if (chunk == 0) {
+        if (resume) hv = a.ws_state[((u0 + nchunk - 1) * a.dim + d) * N + n];
+      } else {
+        hv = a.ws_state[(u0 * a.dim + d) * N + n];
+        for (int j = 1; j < chunk; ++j)
+          hv = fmaf(ex2(rate * a.ws_dt[(u0 + j) * a.dim + d]), hv,
+                    a.ws_state[((u0 + j) * a.dim + d) * N + n]);
       }
-      if (on && SUMMARY && chunk == 0 && resume)
-        a.ws_state[(int64_t(unit + nchunk - 1) * a.dim + d0 + c) * N + n] = hv[k];
     }
-    a01[r] = make_float2(av[0], av[1]);
-    a23[r] = make_float2(av[2], av[3]);
-    h01[r] = make_float2(hv[0], hv[1]);
-    h23[r] = make_float2(hv[2], hv[3]);
-    sdt[r] = 0.f;
+    if (on && SUMMARY && chunk == 0 && resume)
+      a.ws_state[(int64_t(unit + nchunk - 1) * a.dim + d) * N + n] = hv;
+    (k & 1 ? av[k / 2].y : av[k / 2].x) = rate;
+    (k & 1 ? h[k / 2].y : h[k / 2].x) = hv;
   }
   if (SUMMARY && last) return;
+  float sdt = 0.f;
 
   const int64_t t0 = s0 + int64_t(chunk) * a.chunk;
   const int64_t t1 = a.chunk && t0 + a.chunk < s1 ? t0 + a.chunk : s1;
+  const bool gate = !SUMMARY && a.z;
 
-  // staging: the rows and channels of this lane's elements of a stage's tiles
-  constexpr int kLr = CH / EX;  // VEC: lanes per row
-  auto row = [&](int i) { return VEC ? lane / kLr : lane / CH + i * (32 / CH); };
-  auto chn = [&](int i) { return VEC ? lane % kLr * EX + i : lane % CH; };
-  const bool eon = chn(0) < nch;
-  float Dd[EX], bias[EX];
+  // a lane's elements of a stage: rows row0 + i RX, channel (VEC: channels) c0 on
+  const int row0 = VEC ? lane / 2 : lane / CH, c0 = VEC ? lane % 2 * EX : lane % CH;
+  const bool eon = c0 < nch;
+  const int ec = d0 + (eon ? c0 : 0);
+  const int brow0 = VEC ? lane / 2 : NP >= 32 ? 0 : lane / NP;
+  const int bn = VEC ? lane % 2 * EB : NP >= 32 ? lane : lane % NP;
+  const T* px = static_cast<const T*>(a.x) + t0 * a.xs + ec;
+  const TD* pt = static_cast<const TD*>(a.dt) + t0 * a.dts + ec;
+  const T* pz = gate ? static_cast<const T*>(a.z) + t0 * a.zs + ec : nullptr;
+  const T* pb = static_cast<const T*>(a.B) + t0 * a.bs + int64_t(g) * N;
+  const T* pc = static_cast<const T*>(a.C) + t0 * a.cs + int64_t(g) * N;
+  float Dd[VEC ? EX : 1], bias[VEC ? EX : 1];
 #pragma unroll
-  for (int i = 0; i < EX; ++i) {
-    Dd[i] = !SUMMARY && eon && a.D ? a.D[d0 + chn(i)] : 0.f;
-    bias[i] = eon && a.dt_bias ? a.dt_bias[d0 + chn(i)] : 0.f;
+  for (int i = 0; i < (VEC ? EX : 1); ++i) {
+    Dd[i] = !SUMMARY && eon && a.D ? a.D[ec + i] : 0.f;
+    bias[i] = eon && a.dt_bias ? a.dt_bias[ec + i] : 0.f;
   }
-  const T* px = static_cast<const T*>(a.x);
-  const TD* pt = static_cast<const TD*>(a.dt);
-  const T* pz = static_cast<const T*>(a.z);
-  const T* pb = static_cast<const T*>(a.B);
-  const T* pc = static_cast<const T*>(a.C);
   Raw<T, EX, VEC> rx, rz, zc;
   Raw<TD, EX, VEC> rd;
   Raw<T, EB, VEC> rb, rc;
-  float skip[EX];  // D x of the staged tokens
-  // Rows past the end and channels or states past the last read the last one again, and are
-  // masked where they are staged.
-  auto load = [&](int64_t t) {
+  // `left` rows from the stage at the pointers on; rows past them read the last one again
+  auto load = [&](int left) {
     if constexpr (VEC) {
-      const int64_t tt = min(t + row(0), t1 - 1);
-      const int c = d0 + (eon ? chn(0) : 0);
-      rx.load(px + tt * a.xs + c);
-      rd.load(pt + tt * a.dts + c);
-      if (!SUMMARY && pz) rz.load(pz + tt * a.zs + c);
-      constexpr int kLb = NP / EB;  // lanes per row of B and C
-      const int64_t tb = min(t + lane / kLb, t1 - 1);
-      const int n = g * N + lane % kLb * EB;
-      rb.load(pb + tb * a.bs + n);
-      if (!SUMMARY) rc.load(pc + tb * a.cs + n);
+      const int64_t r = min(row0, left - 1);
+      rx.load(px + r * a.xs);
+      rd.load(pt + r * a.dts);
+      if (gate) rz.load(pz + r * a.zs);
+      rb.load(pb + r * a.bs + bn);
+      if (!SUMMARY) rc.load(pc + r * a.cs + bn);
     } else {
 #pragma unroll
       for (int i = 0; i < EX; ++i) {
-        const int64_t tt = min(t + row(i), t1 - 1);
-        const int c = d0 + (eon ? chn(i) : 0);
-        rx.load1(i, px + tt * a.xs + c);
-        rd.load1(i, pt + tt * a.dts + c);
-        if (!SUMMARY && pz) rz.load1(i, pz + tt * a.zs + c);
+        const int64_t r = min(row0 + i * RX, left - 1);
+        rx.load1(i, px + r * a.xs);
+        rd.load1(i, pt + r * a.dts);
+        if (gate) rz.load1(i, pz + r * a.zs);
       }
 #pragma unroll
       for (int i = 0; i < EB; ++i) {
-        const int e = i * 32 + lane;
-        const int64_t tb = min(t + e / NP, t1 - 1);
-        const int n = g * N + min(e % NP, N - 1);
-        rb.load1(i, pb + tb * a.bs + n);
-        if (!SUMMARY) rc.load1(i, pc + tb * a.cs + n);
+        const int64_t r = min(brow0 + i / CB * RB, left - 1);
+        const int n = min(bn + i % CB * 32, N - 1);
+        rb.load1(i, pb + r * a.bs + n);
+        if (!SUMMARY) rc.load1(i, pc + r * a.cs + n);
       }
     }
-  };
-  auto stage = [&](int64_t t) {
-    float xv[EX], dv[EX], bv[EB], cv[EB];
-#pragma unroll
-    for (int i = 0; i < EX; ++i) {
-      const bool on = eon && t + row(i) < t1;  // a row past the end is an identity step
-      xv[i] = on ? rx.get(i) : 0.f;
-      dv[i] = rd.get(i) + bias[i];
-      if (a.softplus) dv[i] = softplus_acc(dv[i]);
-      if (!on) dv[i] = 0.f;
-      skip[i] = Dd[i] * xv[i];
-    }
-    zc = rz;
-#pragma unroll
-    for (int i = 0; i < EB; ++i) {
-      const int e = VEC ? lane * EB + i : i * 32 + lane;
-      const bool on = e % NP < N && t + e / NP < t1;
-      bv[i] = on ? rb.get(i) : 0.f;
-      if (!SUMMARY) cv[i] = on ? rc.get(i) : 0.f;
-    }
-    if constexpr (VEC) {
-      float4* pd = reinterpret_cast<float4*>(du + row(0) * S::kDu + 2 * chn(0));
-      float4* sb = reinterpret_cast<float4*>(bsm + lane * EB);
-      float4* sc = reinterpret_cast<float4*>(csm + lane * EB);
-#pragma unroll
-      for (int i = 0; i < EX; i += 2)
-        pd[i / 2] = make_float4(dv[i], dv[i] * xv[i], dv[i + 1], dv[i + 1] * xv[i + 1]);
-#pragma unroll
-      for (int i = 0; i < EB; i += 4) {
-        sb[i / 4] = make_float4(bv[i], bv[i + 1], bv[i + 2], bv[i + 3]);
-        if (!SUMMARY) sc[i / 4] = make_float4(cv[i], cv[i + 1], cv[i + 2], cv[i + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < EX; ++i) {
-        *reinterpret_cast<float2*>(du + row(i) * S::kDu + 2 * chn(i)) =
-            make_float2(dv[i], dv[i] * xv[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < EB; ++i) {
-        bsm[i * 32 + lane] = bv[i];
-        if (!SUMMARY) csm[i * 32 + lane] = cv[i];
-      }
-    }
-  };
-  auto finish = [&](int64_t t) {  // y of a stage: the gate, the output's type
-    float v[EX];
-#pragma unroll
-    for (int i = 0; i < EX; ++i) {
-      const float* pp = ysm + row(i) * S::kY + S::part(row(i), chn(i));
-      if constexpr (LPC == 2) {
-        const float2 f = *reinterpret_cast<const float2*>(pp);
-        v[i] = skip[i] + (f.x + f.y);
-      } else {
-        const float4 f = *reinterpret_cast<const float4*>(pp);
-        v[i] = skip[i] + ((f.x + f.y) + (f.z + f.w));
-      }
-      if (pz) v[i] *= silu(zc.get(i));
-    }
-    if constexpr (VEC) {
-      if (eon && t + row(0) < t1) {
-        const int64_t at = (t + row(0)) * a.ys + d0 + chn(0);
-        if (a.y_bf16) {
-          uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.y) + at);
-          if constexpr (EX == 4)
-            *reinterpret_cast<uint2*>(to) =
-                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-          else
-            *reinterpret_cast<uint4*>(to) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-        } else {
-          float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
-#pragma unroll
-          for (int i = 0; i < EX; i += 4)
-            to[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < EX; ++i) {
-        if (!eon || t + row(i) >= t1) continue;
-        const int64_t at = (t + row(i)) * a.ys + d0 + chn(i);
-        if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v[i]);
-        else static_cast<float*>(a.y)[at] = v[i];
-      }
-    }
+    px += kStage * a.xs;
+    pt += kStage * a.dts;
+    if (gate) pz += kStage * a.zs;
+    pb += kStage * a.bs;
+    pc += kStage * a.cs;
   };
 
-  constexpr int kGroup = 4;
-  if (t0 < t1) {
-    load(t0);
-    stage(t0);
-  }
-  __syncwarp();
-  for (int64_t t = t0; t < t1; t += TK) {
-    if (t + TK < t1) load(t + TK);
-    const int steps = t1 - t < TK ? int((t1 - t + kGroup - 1) / kGroup) : TK / kGroup;
-    // kGroup tokens at a time, the next ones' operands on their way while these are worked on
-    float4 bn[kGroup], cn[kGroup];
-    float2 dn[kGroup][R];
-    auto fetch = [&](int k0) {
+  int64_t left64 = t1 - t0;
+  int left = left64 > kStage ? kStage : int(left64);  // rows of the current stage
+  if (left > 0) load(left);
+  int64_t yrow = t0 * a.ys;
+  for (; left64 > 0; left64 -= kStage) {
+    left = left64 > kStage ? kStage : int(left64);
+    float skip[EX];
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        bn[i] = *reinterpret_cast<const float4*>(bsm + (k0 + i) * NP + q * 4);
-        if (!SUMMARY) cn[i] = *reinterpret_cast<const float4*>(csm + (k0 + i) * NP + q * 4);
+    for (int i = 0; i < EX; i += (EX > 1 ? 2 : 1)) {
+      float2 v2;
+      float xv[2], dv[2];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          dn[i][r] =
-              *reinterpret_cast<const float2*>(du + (k0 + i) * S::kDu + 2 * (cg * R + r));
+      for (int e = 0; e < (EX > 1 ? 2 : 1); ++e) {
+        xv[e] = rx.get(i + e);
+        dv[e] = rd.get(i + e) + bias[VEC ? i + e : 0];
+        skip[i + e] = Dd[VEC ? i + e : 0] * xv[e];
       }
-    };
-    fetch(0);
-    for (int k4 = 0; k4 < steps; ++k4) {
-      float4 bv[kGroup], cv[kGroup];
-      float2 dv[kGroup][R];
+      if (EX == 1) dv[1] = xv[1] = 0.f;
+      v2 = make_float2(dv[0], dv[1]);
+      if (a.softplus) v2 = softplus_acc2(v2);
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        bv[i] = bn[i];
-        if (!SUMMARY) cv[i] = cn[i];
-#pragma unroll
-        for (int r = 0; r < R; ++r) dv[i][r] = dn[i][r];
+      for (int e = 0; e < (EX > 1 ? 2 : 1); ++e) {
+        // rows past the end are identity steps
+        const bool on = eon && row0 + (i + e) * RX < left;
+        const float v = on ? (e ? v2.y : v2.x) : 0.f;
+        const int k = row0 + (i + e) * RX;
+        du[k * CH + place(k, c0 + (VEC ? i + e : 0))] = make_float2(v, on ? v * xv[e] : 0.f);
       }
-      if (k4 + 1 < steps) fetch((k4 + 1) * kGroup);
-      float pv[kGroup][R];
+    }
+    zc = rz;
+    if constexpr (VEC) {
+      const bool on = brow0 < left;
+#pragma unroll
+      for (int i = 0; i < EB; i += 4) {
+        *reinterpret_cast<float4*>(bsm + lane * EB + i) =
+            on ? make_float4(rb.get(i), rb.get(i + 1), rb.get(i + 2), rb.get(i + 3))
+               : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!SUMMARY)
+          *reinterpret_cast<float4*>(csm + lane * EB + i) =
+              on ? make_float4(rc.get(i), rc.get(i + 1), rc.get(i + 2), rc.get(i + 3))
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EB; ++i) {
+        const bool on = bn + i % CB * 32 < N && brow0 + i / CB * RB < left;
+        bsm[i * 32 + lane] = on ? rb.get(i) : 0.f;
+        if (!SUMMARY) csm[i * 32 + lane] = on ? rc.get(i) : 0.f;
+      }
+    }
+    __syncwarp();
+    if (left64 > kStage) load(left64 - kStage > kStage ? kStage : int(left64) - kStage);
+
+    // the steps, kGroup tokens unrolled
+    constexpr int kGroup = 8;
+#pragma unroll 1
+    for (int k0 = 0; k0 < left; k0 += kGroup) {
+      float p[kGroup];
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
+        const int k = k0 + i;
+        const float2 v = du[k * CH + place(k, ch)];
+        const float2 dd = dup(v.x), uu = dup(v.y);
+        float2 acc = dup(0.f);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float2 dd = make_float2(dv[i][r].x, dv[i][r].x);
-          const float2 uu = make_float2(dv[i][r].y, dv[i][r].y);
-          const float2 l01 = mul2(dd, a01[r]), l23 = mul2(dd, a23[r]);
-          h01[r] = fma2(make_float2(ex2(l01.x), ex2(l01.y)), h01[r],
-                        mul2(uu, make_float2(bv[i].x, bv[i].y)));
-          h23[r] = fma2(make_float2(ex2(l23.x), ex2(l23.y)), h23[r],
-                        mul2(uu, make_float2(bv[i].z, bv[i].w)));
-          if (SUMMARY) {
-            sdt[r] += dd.x;
-          } else {
-            const float2 p2 = fma2(make_float2(cv[i].z, cv[i].w), h23[r],
-                                   mul2(make_float2(cv[i].x, cv[i].y), h01[r]));
-            pv[i][r] = p2.x + p2.y;
+        for (int m = 0; m < P; m += 2) {
+          const float4 bv = *reinterpret_cast<const float4*>(bsm + k * NP + q * SPL + 2 * m);
+          const float2 l0 = mul2(dd, av[m]), l1 = mul2(dd, av[m + 1]);
+          h[m] = fma2(make_float2(ex2(l0.x), ex2(l0.y)), h[m], mul2(uu, make_float2(bv.x, bv.y)));
+          h[m + 1] = fma2(make_float2(ex2(l1.x), ex2(l1.y)), h[m + 1],
+                          mul2(uu, make_float2(bv.z, bv.w)));
+          if (!SUMMARY) {
+            const float4 cv = *reinterpret_cast<const float4*>(csm + k * NP + q * SPL + 2 * m);
+            acc = m == 0 ? mul2(make_float2(cv.x, cv.y), h[0])
+                         : fma2(make_float2(cv.x, cv.y), h[m], acc);
+            acc = fma2(make_float2(cv.z, cv.w), h[m + 1], acc);
           }
         }
+        if (SUMMARY) sdt += v.x;
+        p[i] = acc.x + acc.y;
       }
       if (!SUMMARY) {
+        // the lanes' sums meet in shared memory, added when the stage's y is finished
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float p = pv[i][r];
-#pragma unroll
-            for (int o = 4; o < LPC; o <<= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-            // the lanes' sums meet in shared memory, added when the stage's y is finished
-            if (LPC <= 4 || q < 4)
-              ysm[(k4 * kGroup + i) * S::kY + S::part(i, cg * R + r) + q] = p;
-          }
+        for (int i = 0; i < kGroup; ++i) ysm[(k0 + i) * 32 + place(k0 + i, ch) * LPC + q] = p[i];
       }
     }
     __syncwarp();
     if (!SUMMARY) {
-      finish(t);
-      __syncwarp();
+      float v[EX];
+#pragma unroll
+      for (int i = 0; i < EX; ++i) {
+        const int k = row0 + i * RX;
+        const float* pp = ysm + k * 32 + place(k, c0 + (VEC ? i : 0)) * LPC;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < LPC; e += LPC < 4 ? LPC : 4) {
+          if constexpr (LPC == 2) {
+            const float2 f = *reinterpret_cast<const float2*>(pp);
+            sum = f.x + f.y;
+          } else {
+            const float4 f = *reinterpret_cast<const float4*>(pp + e);
+            sum += (f.x + f.y) + (f.z + f.w);
+          }
+        }
+        v[i] = skip[i] + sum;
+      }
+      if (gate) {
+#pragma unroll
+        for (int i = 0; i < EX; i += (EX > 1 ? 2 : 1)) {
+          const float2 zz = make_float2(zc.get(i), EX > 1 ? zc.get(i + (EX > 1)) : 0.f);
+          const float2 g2 = mul2(zz, sigmoid2(zz));
+          v[i] *= g2.x;
+          if (EX > 1) v[i + (EX > 1)] *= g2.y;
+        }
+      }
+      if constexpr (VEC) {
+        if (eon && row0 < left) {
+          const int64_t to = yrow + row0 * a.ys + ec;
+          if (a.y_bf16) {
+            uint32_t w[EX / 2];
+#pragma unroll
+            for (int i = 0; i < EX; i += 2) w[i / 2] = pack_bf16x2(v[i], v[i + 1]);
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.y) + to;
+            if constexpr (EX == 8)
+              *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < EX; i += 4)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.y) + to + i) =
+                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < EX; ++i) {
+          if (!eon || row0 + i * RX >= left) continue;
+          const int64_t to = yrow + (row0 + i * RX) * a.ys + ec;
+          if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v[i]);
+          else static_cast<float*>(a.y)[to] = v[i];
+        }
+      }
+      yrow += kStage * a.ys;
     }
-    if (t + TK < t1) stage(t + TK);
-    __syncwarp();
   }
 
   // the state after the unit
+  if (SUMMARY && con && q == 0) a.ws_dt[int64_t(unit) * a.dim + d] = sdt;
+  if (!con || (!SUMMARY && (!last || !a.state || (s0 == s1 && resume)))) return;
+  float* to = SUMMARY ? a.ws_state + (int64_t(unit) * a.dim + d) * N
+                      : a.state + (slot * a.dim + d) * N;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int c = cg * R + r;
-    if (c >= nch) continue;
-    float* to = nullptr;
-    if (SUMMARY) {
-      to = a.ws_state + (int64_t(unit) * a.dim + d0 + c) * N;
-      if (q == 0) a.ws_dt[int64_t(unit) * a.dim + d0 + c] = sdt[r];
-    } else if (last && a.state && !(s0 == s1 && resume)) {
-      to = a.state + (slot * a.dim + d0 + c) * N;
-    }
-    if (!to) continue;
-    const float hv[4] = {h01[r].x, h01[r].y, h23[r].x, h23[r].y};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (q * 4 + k < N) to[q * 4 + k] = hv[k];
-  }
+  for (int k = 0; k < SPL; ++k)
+    if (q * SPL + k < N) to[q * SPL + k] = k & 1 ? h[k / 2].y : h[k / 2].x;
 }
 
 // One token of each sequence.  LPC lanes per channel with 4 states each, a warp on 32 / LPC
