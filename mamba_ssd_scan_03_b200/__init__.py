@@ -15,6 +15,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssd.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 SSD_F32, SSD_BF16 = 0, 1
 SSD_PATH_SIMT, SSD_PATH_TCGEN05 = 0, 1
@@ -533,107 +534,26 @@ def step(state, x, dt, A, B, C, D, out=None, y_dtype=torch.float32):
 
 
 # ---- packed prompts and single tokens with caches, and the group norm -------------------------
+# Checked and launched by the compiled binding (csrc/binding.cpp): a token's call is mostly host
+# time.
+
+_served = None
 
 
-def _row_stride(t, name, dtype, shape, device):
-    """Check a tensor of packed rows (any row stride, the values of a row contiguous) and give its
-    row stride in elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
-        return width
-    stride, width = t.stride(), 1
-    for k in range(len(shape) - 1, 0, -1):
-        if shape[k] != 1 and stride[k] != width:
-            raise ValueError(f"the values of a row of {name} must be contiguous")
-        width *= shape[k]
-    if shape[0] <= 1:
-        return width
-    if stride[0] < width:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return stride[0]
-
-
-def _whole(t, name, dtype, shape, device):
-    """Check a contiguous tensor and give its address; a None stays None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _first(t, name, ndim):
-    """Check the tensor whose device and shape the others follow; gives its device's index."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
-    return t.get_device()
-
-
-# The raw handle of a device's current stream: a small call's time is largely its host time, and
-# building a Stream object for the handle alone costs 3 us of it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _launch(fn, dev, *args):
-    """Call a C entry with device `dev` current, on its current stream."""
-    if torch.cuda.current_device() == dev:
-        rc = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev))
-    if rc != 0:
-        raise SSDError(rc, fn.__name__)
-
-
-def _seqs(cu_seqlens, resume, dev):
-    """Pointers of a packed batch's bounds [nseq + 1] int32 and flags [nseq] (bool or uint8)."""
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or \
-            cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must be a tensor of nseq + 1 bounds")
-    nseq = cu_seqlens.shape[0] - 1
-    cu = _whole(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
-    if resume is None:
-        return nseq, cu, None
-    if not isinstance(resume, torch.Tensor) or resume.dtype not in (torch.bool, torch.uint8):
-        raise TypeError("resume must be a bool or uint8 tensor")
-    return nseq, cu, _whole(resume, "resume", resume.dtype, (nseq,), dev)
-
-
-def _conv_cache(conv_state, dtype, Cd, K, dev):
-    if conv_state is None:
-        return None, 0
-    if not isinstance(conv_state, torch.Tensor) or conv_state.dim() != 3:
-        raise ValueError("conv_state must be a tensor [nslots, K-1, C]")
-    nslots = conv_state.shape[0]
-    p = _whole(conv_state, "conv_state", dtype, (nslots, K - 1, Cd), dev)
-    return (None, 0) if K == 1 else (p, nslots)
-
-
-def _kernel_width(w, Cd):
-    if not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise ValueError("w must be a tensor [C, K]")
-    return w.shape[1]
+def _call(name, *args):
+    global _served
+    if _served is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -m mamba_ssd_scan_03_b200.build`")
+        from . import _binding
+        _binding.bind(LIB_PATH)
+        _served = _binding
+    out = getattr(_served, name)(*args)
+    if out.__class__ is int:
+        raise SSDError(out, "ssd_" + name)
+    return out
 
 
 def conv_silu_varlen(u, w, cu_seqlens, bias=None, conv_state=None, slots=None, resume=None,
@@ -647,78 +567,13 @@ def conv_silu_varlen(u, w, cu_seqlens, bias=None, conv_state=None, slots=None, r
     [nseq] bool says which sequences continue from their slot (None: none).  Rows outside the
     sequences are not written.  Bad slots and bounds are left out and reported by
     device_status()."""
-    dev = _first(u, "u", 2)
-    T, Cd = u.shape
-    K = _kernel_width(w, Cd)
-    io = _io(u)
-    us = _row_stride(u, "u", None, (T, Cd), dev)
-    nseq, cu, res = _seqs(cu_seqlens, resume, dev)
-    state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
-    if out is None:
-        out = u.new_empty((T, Cd))
-    os_ = _row_stride(out, "out", u.dtype, (T, Cd), dev)
-    _launch(load().ssd_conv_silu_varlen, dev, u.data_ptr(), us,
-            _whole(w, "w", torch.float32, (Cd, K), dev),
-            _whole(bias, "bias", torch.float32, (Cd,), dev), cu, state,
-            _whole(slots, "slots", torch.int32, (nseq,), dev), res, out.data_ptr(), os_, T, nseq,
-            nslots, Cd, K, io)
-    return out
+    return _call("conv_silu_varlen", u, w, cu_seqlens, bias, conv_state, slots, resume, out)
 
 
 def conv_silu_step(conv_state, u, w, bias=None, slots=None, out=None):
     """conv_silu_varlen for one token of each sequence: u [batch,C] -> out [batch,C]; conv_state
     [nslots,K-1,C] is read and moved on in place (K 2..8)."""
-    dev = _first(u, "u", 2)
-    Bt, Cd = u.shape
-    K = _kernel_width(w, Cd)
-    io = _io(u)
-    us = _row_stride(u, "u", None, (Bt, Cd), dev)
-    state, nslots = _conv_cache(conv_state, u.dtype, Cd, K, dev)
-    if out is None:
-        out = u.new_empty((Bt, Cd))
-    os_ = _row_stride(out, "out", u.dtype, (Bt, Cd), dev)
-    _launch(load().ssd_conv_silu_step, dev, state, u.data_ptr(), us,
-            _whole(w, "w", torch.float32, (Cd, K), dev),
-            _whole(bias, "bias", torch.float32, (Cd,), dev),
-            _whole(slots, "slots", torch.int32, (Bt,), dev), out.data_ptr(), os_, Bt, nslots, Cd,
-            K, io)
-    return out
-
-
-def _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, nseq, out, y_dtype):
-    dev = _first(x, "x", 2)
-    rows, dim = x.shape
-    io = _io(x)
-    if not isinstance(A, torch.Tensor) or A.dim() != 2:
-        raise ValueError("A must be a tensor [dim, dstate]")
-    if not isinstance(B, torch.Tensor) or B.dim() != 3:
-        raise ValueError("B must be a tensor [rows, G, dstate]")
-    if not isinstance(dt, torch.Tensor):
-        raise TypeError("dt must be a torch.Tensor")
-    N, G = A.shape[1], B.shape[1]
-    if dt.dtype != torch.float32 and dt.dtype != x.dtype:
-        raise TypeError(f"dt must be float32 or {x.dtype}, got {dt.dtype}")
-    shape, bc = (rows, dim), (rows, G, N)
-    y_dtype = out.dtype if out is not None else y_dtype
-    y = x.new_empty(shape, dtype=y_dtype) if out is None else out
-    nslots = 0
-    if state is not None:
-        if not isinstance(state, torch.Tensor) or state.dim() != 3:
-            raise ValueError("state must be a tensor [nslots, dim, dstate]")
-        nslots = state.shape[0]
-    strides = (_row_stride(x, "x", None, shape, dev), _row_stride(dt, "dt", None, shape, dev),
-               _row_stride(B, "B", x.dtype, bc, dev), _row_stride(C, "C", x.dtype, bc, dev),
-               0 if z is None else _row_stride(z, "z", x.dtype, shape, dev),
-               _row_stride(y, "out", y_dtype, shape, dev))
-    args = SelectiveArgs(
-        x.data_ptr(), dt.data_ptr(), _whole(A, "A", torch.float32, (dim, N), dev), B.data_ptr(),
-        C.data_ptr(), _whole(D, "D", torch.float32, (dim,), dev),
-        _whole(dt_bias, "dt_bias", torch.float32, (dim,), dev),
-        None if z is None else z.data_ptr(), y.data_ptr(),
-        _whole(state, "state", torch.float32, (nslots, dim, N), dev),
-        _whole(slots, "slots", torch.int32, (rows if nseq is None else nseq,), dev), *strides,
-        nslots, dim, N, G, io, _code(dt.dtype), _code(y_dtype), 1 if softplus else 0)
-    return dev, args, y
+    return _call("conv_silu_step", conv_state, u, w, bias, slots, out)
 
 
 def selective_varlen_workspace_size(ntok, nseq, dim, dstate, ngroups, max_seqlen=0):
@@ -736,33 +591,16 @@ def selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=No
     dt + dt_bias goes through a softplus when `softplus` is set; z, where given, gates y with
     silu(z).  state [nslots,dim,N] f32, slots and resume as conv_state, slots and resume of
     conv_silu_varlen.  max_seqlen (0: unknown) only helps to choose the plan."""
-    nseq, cu, res = _seqs(cu_seqlens, resume, _first(x, "x", 2))
-    dev, args, y = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, nseq,
-                                   out, y_dtype)
-    lib = load()
-    T, ws, need = x.shape[0], None, 0
-    if nseq > 0:
-        need = lib.ssd_selective_varlen_workspace_size(T, nseq, args.dim, args.dstate,
-                                                       args.ngroups, max_seqlen)
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, device=x.device)
-        ws, need = workspace.data_ptr(), workspace.numel()
-    elif need > 0:
-        workspace = x.new_empty((need,), dtype=torch.uint8)
-        ws = workspace.data_ptr()
-    _launch(lib.ssd_selective_scan_varlen, dev, ctypes.byref(args), cu, res, T, nseq, max_seqlen,
-            ws, need)
-    return y
+    return _call("selective_scan_varlen", x, dt, A, B, C, D, z, dt_bias, softplus, state, slots,
+                 out, y_dtype, cu_seqlens, resume, max_seqlen, workspace)
 
 
 def selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
                    slots=None, out=None, y_dtype=torch.float32):
     """selective_scan_varlen for one token of each sequence: x, dt, z [batch,dim], B, C
     [batch,G,N]; state [nslots,dim,N] f32 is updated in place at each row's slot."""
-    dev, args, y = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, None,
-                                   out, y_dtype)
-    _launch(load().ssd_selective_step, dev, ctypes.byref(args), x.shape[0])
-    return y
+    return _call("selective_step", x, dt, A, B, C, D, z, dt_bias, softplus, state, slots, out,
+                 y_dtype)
 
 
 def group_norm_gate(y, weight, bias=None, z=None, ngroups=1, eps=1e-5, center=False,
@@ -773,48 +611,17 @@ def group_norm_gate(y, weight, bias=None, z=None, ngroups=1, eps=1e-5, center=Fa
     v = y silu(z) (gate_first) or y; out = (v - mean) / sqrt(mean((v - mean)^2) + eps) weight +
     bias per group of C / ngroups channels, times silu(z) when the gate comes last; the mean is
     taken as 0 unless `center` is set (RMS norm)."""
-    dev = _first(y, "y", 2)
-    rows, Cd = y.shape
-    shape = (rows, Cd)
-    out_dtype = out.dtype if out is not None else out_dtype
-    if out is None:
-        out = y.new_empty(shape, dtype=out_dtype)
-    zs = 0 if z is None else _row_stride(z, "z", None, shape, dev)
-    os_ = _row_stride(out, "out", out_dtype, shape, dev)
-    _launch(load().ssd_group_norm_gate, dev, y.data_ptr(), _row_stride(y, "y", None, shape, dev),
-            _whole(weight, "weight", torch.float32, (Cd,), dev),
-            _whole(bias, "bias", torch.float32, (Cd,), dev), _ptr(z), zs, out.data_ptr(), os_, rows, Cd, ngroups, eps, bool(center),
-            bool(gate_first), _code(y.dtype), SSD_F32 if z is None else _code(z.dtype),
-            _code(out_dtype))
-    return out
+    return _call("group_norm_gate", y, weight, bias, z, ngroups, eps, center, gate_first, out,
+                 out_dtype)
 
 
 def group_norm_gate_bwd(dout, y, weight, bias=None, z=None, ngroups=1, eps=1e-5, center=False,
                         gate_first=True, workspace=None):
     """Gradients of L = sum(dout * out) through group_norm_gate.  Returns a dict: y [rows,C] f32,
     z [rows,C] in z's dtype (or None), weight [C] f32, bias [C] f32 (or None)."""
-    lib = load()
-    dev = _first(y, "y", 2)
-    rows, Cd = y.shape
-    shape = (rows, Cd)
-    strides = [_row_stride(t, n, None, shape, dev) for t, n in ((dout, "dout"), (y, "y"))]
-    zs = 0 if z is None else _row_stride(z, "z", None, shape, dev)
-    wp = _whole(weight, "weight", torch.float32, (Cd,), dev)
-    bp = _whole(bias, "bias", torch.float32, (Cd,), dev)
-    g = {"y": y.new_empty(shape, dtype=torch.float32),
-         "z": None if z is None else z.new_empty(shape),
-         "weight": weight.new_empty((Cd,)),
-         "bias": None if bias is None else weight.new_empty((Cd,))}
-    if workspace is None:
-        need = lib.ssd_group_norm_gate_bwd_workspace_size(rows, Cd, ngroups)
-        workspace = y.new_empty((max(need, 1),), dtype=torch.uint8)
-    _need(workspace, "workspace", torch.uint8, device=y.device)
-    _launch(lib.ssd_group_norm_gate_bwd, dev, dout.data_ptr(), strides[0], y.data_ptr(),
-            strides[1], wp, bp, _ptr(z), zs, g["y"].data_ptr(), _ptr(g["z"]),
-            g["weight"].data_ptr(), _ptr(g["bias"]), rows, Cd, ngroups, eps, bool(center),
-            bool(gate_first), _code(dout.dtype), _code(y.dtype),
-            SSD_F32 if z is None else _code(z.dtype), workspace.data_ptr(), workspace.numel())
-    return g
+    return dict(zip(("y", "z", "weight", "bias"),
+                    _call("group_norm_gate_bwd", y, weight, bias, z, ngroups, eps, center,
+                          gate_first, dout, workspace)))
 
 
 def device_status(device=None):

@@ -1,8 +1,9 @@
-"""Build libssd.so (the sm_100a CUDA library behind include/ssd.h) in-tree.
+"""Build libssd.so (the sm_100a CUDA library behind include/ssd.h) and _binding.so (the Python
+binding of its served forms) in-tree.
 
 ``python -m mamba_ssd_scan_03_b200.build`` or ``build()``.  One nvcc invocation on the single
-translation unit ``csrc/ssd_lib.cu``; the .so lands next to this file so it travels with the
-repository snapshot and the binding loads it from here.
+translation unit ``csrc/ssd_lib.cu`` and one of the host compiler on ``csrc/binding.cpp``; both land
+next to this file so that they travel with the repository snapshot and are loaded from here.
 """
 import os
 import subprocess
@@ -13,6 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssd.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+BINDING = os.path.join(HERE, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -31,7 +34,32 @@ def up_to_date(path, deps):
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def build_binding(force=False, verbose=False):
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and up_to_date(BINDING, [src, os.path.join(ROOT, "include", "ssd.h")]):
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    include = [os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{p}" for p in include], src, "-L" + os.path.join(base, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force=False, verbose=False, ptxas_info=False):
+    build_binding(force, verbose)
     deps = sources()
     if not force and up_to_date(LIB, deps):
         return LIB
