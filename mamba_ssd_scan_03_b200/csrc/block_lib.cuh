@@ -244,11 +244,11 @@ ssd_status launch_sel(const ssd::cache::SelArgs& k, const SelPlan& p, cudaStream
   if (p.units * ncb > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   const unsigned grid = unsigned(p.units * ncb);
   if (k.chunk) {
-    cc::selective_varlen_kernel<T, TD, LPC, SPL, VEC, true><<<grid, 32, 0, stream>>>(k);
+    cc::selective_varlen_kernel<T, TD, LPC, SPL, VEC, true><<<grid, 64, 0, stream>>>(k);
     const ssd_status st = launched();
     if (st != SSD_OK) return st;
   }
-  cc::selective_varlen_kernel<T, TD, LPC, SPL, VEC, false><<<grid, 32, 0, stream>>>(k);
+  cc::selective_varlen_kernel<T, TD, LPC, SPL, VEC, false><<<grid, 64, 0, stream>>>(k);
   return launched();
 }
 // Wide loads take whole rows of 8 or 16 states and channel groups that start and end on a lane's

@@ -49,33 +49,29 @@ __device__ __forceinline__ float rate2(float a) {
   return r < -1e38f ? -1e38f : r;
 }
 
-// softplus(v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1]: no exponential overflows, and
-// small results keep their relative accuracy: log(1 + e) = 2 atanh(w), w = e / (2 + e) <= 1/3,
-// by the odd series w + w^3/3 + w^5/5 + ...; the terms past w^13 / 13 are below 2^-25 of it.
+// softplus(v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1]: no exponential overflows.  log(1 + e) =
+// e p(e) keeps the relative accuracy of small results; p is the Chebyshev interpolant of degree 9
+// of log(1 + e) / e on [0, 1] (off by 5e-9; with its float32 arithmetic by 1.3e-7).
+__device__ __forceinline__ constexpr float log1p_coef(int k) {
+  constexpr float c[10] = {1.f,           -0.499998927f, 0.333297104f,  -0.249516159f,
+                           0.196632743f,  -0.152696669f, 0.105436236f,  -0.0563736111f,
+                           0.0195425265f, -0.00317605701f};
+  return c[k];
+}
 __device__ __forceinline__ float softplus_acc(float v) {
   const float e = ex2(-fabsf(v) * kLog2e);
-  const float w = e * rcp(2.f + e), s = w * w;
-  float p = fmaf(s, 1.f / 13.f, 1.f / 11.f);
-  p = fmaf(s, p, 1.f / 9.f);
-  p = fmaf(s, p, 1.f / 7.f);
-  p = fmaf(s, p, 1.f / 5.f);
-  p = fmaf(s, p, 1.f / 3.f);
-  const float w2 = w + w;
-  return fmaxf(v, 0.f) + fmaf(w2 * s, p, w2);
+  float p = log1p_coef(9);
+#pragma unroll
+  for (int k = 8; k >= 0; --k) p = fmaf(p, e, log1p_coef(k));
+  return fmaf(p, e, fmaxf(v, 0.f));
 }
-
 // The same of a pair.
 __device__ __forceinline__ float2 softplus_acc2(float2 v) {
   const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
-  const float2 b = add2(e, dup(2.f));
-  const float2 w = mul2(e, make_float2(rcp(b.x), rcp(b.y))), s = mul2(w, w);
-  float2 p = fma2(s, dup(1.f / 13.f), dup(1.f / 11.f));
-  p = fma2(s, p, dup(1.f / 9.f));
-  p = fma2(s, p, dup(1.f / 7.f));
-  p = fma2(s, p, dup(1.f / 5.f));
-  p = fma2(s, p, dup(1.f / 3.f));
-  const float2 w2 = add2(w, w);
-  return add2(make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)), fma2(mul2(w2, s), p, w2));
+  float2 p = dup(log1p_coef(9));
+#pragma unroll
+  for (int k = 8; k >= 0; --k) p = fma2(p, e, dup(log1p_coef(k)));
+  return fma2(p, e, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
 // NV neighbouring values of a row as they lie in memory (one or two wide accesses), or one value
@@ -109,27 +105,33 @@ struct Raw {
   }
 };
 
-// One warp scans one unit: a sequence (chunk == 0) or a chunk of one, for 32 / LPC channels of
+// Two warps scan one unit: a sequence (chunk == 0) or a chunk of one, for 32 / LPC channels of
 // one group; LPC lanes per channel hold SPL of its states each.  SUMMARY: only the state after
 // the chunk, from zero (or, for a sequence's first chunk, from the sequence's initial state), and
 // the chunk's sum of dt; those give the scan of a later chunk its entering state,
 // h <- exp(A sum_dt) h + S chunk by chunk.
 //
-// Tokens come in stages of 16: the next stage's values are loaded into registers ahead of the
-// current stage's steps, then converted (softplus, dt x, D x) once per element into shared memory,
-// where the lanes of a channel read them.  VEC: a lane loads EX neighbouring channels of one row
-// (and EB neighbouring states) in one access, which asks for rows of 16-byte multiples; else
-// neighbouring lanes load neighbouring channels one by one.  Nothing branches between a load and
-// its use, and addresses are a pointer per input that moves on by a stage: with one or two warps
-// to a scheduler every instruction outside the steps is time of its own.
+// Tokens come in stages of 16.  One warp steps through a stage's tokens; meanwhile the other
+// prepares the next stage (converts the loaded values, softplus, dt x, D x, into shared memory),
+// loads the one after it into registers, and finishes the stage before (adds the lanes' sums,
+// gate, output).  They meet at one barrier a stage.  Done by one warp, one after the other, the
+// preparation costs a third of the time wherever a scheduler has a single sequence to work on.
+// VEC: a lane loads EX neighbouring channels of one row (and EB neighbouring states) in one
+// access, which asks for rows of 16-byte multiples; else neighbouring lanes load neighbouring
+// channels one by one.  Nothing branches between a load and its use, and addresses are a pointer
+// per input that moves on by a stage.
 // Why two lanes per channel for 16 states: reading B and C fills registers at 128 bytes a clock
 // and SM, or 256 where a warp reads one or two addresses, and every lane reads its states' B and
 // C anew; with four lanes of four states that takes longer than the exponentials.
-constexpr int kStage = 16;
+constexpr int kStage = 16, kAhead = 2;
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 template <typename T, typename TD, int LPC, int SPL, bool VEC, bool SUMMARY>
-__global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
-  constexpr int CH = 32 / LPC;         // channels of a warp
+__global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
+  constexpr int CH = 32 / LPC;         // channels of the unit
   constexpr int NP = LPC * SPL;        // states, padded
   constexpr int EX = CH / 2;           // x, dt, z elements per lane and stage
   constexpr int EB = NP / 2;           // B, C elements per lane and stage
@@ -137,15 +139,27 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
   constexpr int RX = VEC ? 0 : 32 / CH;  // rows between a lane's elements
   constexpr int RB = VEC ? 0 : (NP >= 32 ? 1 : 32 / NP);
   constexpr int CB = NP / 32 > 1 ? NP / 32 : 1;  // B, C elements of a row per lane
-  // arrays of their own, so that the compiler may move loads of one over stores to another
-  __shared__ __align__(16) float2 du[kStage * CH];
-  __shared__ __align__(16) float bsm[kStage * NP], csm[SUMMARY ? 4 : kStage * NP];
-  __shared__ __align__(16) float ysm[SUMMARY ? 4 : kStage * 32];
+  // two stages each; arrays of their own, so that the compiler may move loads of one over stores
+  // to another
+  __shared__ __align__(16) float2 du[2][kStage * CH];
+  __shared__ __align__(16) float bsm[2][kStage * NP], csm[2][SUMMARY ? 4 : kStage * NP];
+  __shared__ __align__(16) float ysm[2][SUMMARY ? 4 : kStage * 32];
   // place of channel c in the rows of token k: what lanes on the same channels of eight rows touch
   // together lies on banks of its own
   auto place = [](int k, int c) { return c ^ (k & (CH < 8 ? CH - 1 : 7)); };
 
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  // Which warp steps and which prepares.  CTAs of two warps take the SM's four schedulers in fixed
+  // pairs, so that "the first warp" would be on the same two in all of them; taking turns by the
+  // hardware's warp slot spreads the stepping warps (and their exponentials) over all four.
+  __shared__ int first_steps;
+  if (threadIdx.x == 0) {
+    unsigned slot_id;
+    asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot_id));
+    first_steps = !(slot_id >> 2 & 1);
+  }
+  __syncthreads();
+  const bool steps = (threadIdx.x < 32) == bool(first_steps);
   const int dpg = a.dim / a.ngroups;
   const int cpg = (dpg + CH - 1) / CH;  // channel blocks per group
   const unsigned ncb = unsigned(cpg) * a.ngroups;
@@ -195,45 +209,101 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
   const bool last = chunk == nchunk - 1;
   const bool resume = a.state && a.resume && a.resume[seq];
 
-  // this lane's channel, states and constants
-  const int q = lane % LPC, ch = lane / LPC;
-  const bool con = ch < nch;
-  const int d = d0 + (con ? ch : 0);
-  float2 av[P], h[P];
-#pragma unroll
-  for (int k = 0; k < SPL; ++k) {
-    const int n = q * SPL + k;
-    const bool on = con && n < N;
-    const float rate = on ? rate2(a.A[int64_t(d) * N + n]) : 0.f;
-    float hv = 0.f;
-    if (on && resume && chunk == 0 && (SUMMARY || nchunk == 1))
-      hv = a.state[(slot * a.dim + d) * N + n];
-    if (on && !SUMMARY && nchunk > 1) {
-      // a sequence cut into chunks: its initial state was copied by the summary launch (the last
-      // chunk may already have moved the slot's), the others' follow from the summaries
-      const int64_t u0 = unit - chunk;
-      if (chunk == 0) {
-        if (resume) hv = a.ws_state[((u0 + nchunk - 1) * a.dim + d) * N + n];
-      } else {
-        hv = a.ws_state[(u0 * a.dim + d) * N + n];
-        for (int j = 1; j < chunk; ++j)
-          hv = fmaf(ex2(rate * a.ws_dt[(u0 + j) * a.dim + d]), hv,
-                    a.ws_state[((u0 + j) * a.dim + d) * N + n]);
-      }
-    }
-    if (on && SUMMARY && chunk == 0 && resume)
-      a.ws_state[(int64_t(unit + nchunk - 1) * a.dim + d) * N + n] = hv;
-    (k & 1 ? av[k / 2].y : av[k / 2].x) = rate;
-    (k & 1 ? h[k / 2].y : h[k / 2].x) = hv;
-  }
-  if (SUMMARY && last) return;
-  float sdt = 0.f;
-
+  if (SUMMARY && last) return;  // no chunk after it asks
   const int64_t t0 = s0 + int64_t(chunk) * a.chunk;
   const int64_t t1 = a.chunk && t0 + a.chunk < s1 ? t0 + a.chunk : s1;
-  const bool gate = !SUMMARY && a.z;
+  const int64_t rows = t1 - t0;
+  const int64_t nst = (rows + kStage - 1) / kStage;
 
-  // a lane's elements of a stage: rows row0 + i RX, channel (VEC: channels) c0 on
+  if (steps) {
+    // this lane's channel, states and rates
+    const int q = lane % LPC, ch = lane / LPC;
+    const bool con = ch < nch;
+    const int d = d0 + (con ? ch : 0);
+    float2 av[P], h[P];
+#pragma unroll
+    for (int k = 0; k < SPL; ++k) {
+      const int n = q * SPL + k;
+      const bool on = con && n < N;
+      const float rate = on ? rate2(a.A[int64_t(d) * N + n]) : 0.f;
+      float hv = 0.f;
+      if (on && resume && chunk == 0 && (SUMMARY || nchunk == 1))
+        hv = a.state[(slot * a.dim + d) * N + n];
+      if (on && !SUMMARY && nchunk > 1) {
+        // a sequence cut into chunks: its initial state was copied by the summary launch (the
+        // last chunk may already have moved the slot's), the others' follow from the summaries
+        const int64_t u0 = unit - chunk;
+        if (chunk == 0) {
+          if (resume) hv = a.ws_state[((u0 + nchunk - 1) * a.dim + d) * N + n];
+        } else {
+          hv = a.ws_state[(u0 * a.dim + d) * N + n];
+          for (int j = 1; j < chunk; ++j)
+            hv = fmaf(ex2(rate * a.ws_dt[(u0 + j) * a.dim + d]), hv,
+                      a.ws_state[((u0 + j) * a.dim + d) * N + n]);
+        }
+      }
+      if (on && SUMMARY && chunk == 0 && resume)
+        a.ws_state[(int64_t(unit + nchunk - 1) * a.dim + d) * N + n] = hv;
+      (k & 1 ? av[k / 2].y : av[k / 2].x) = rate;
+      (k & 1 ? h[k / 2].y : h[k / 2].x) = hv;
+    }
+    float sdt = 0.f;
+    __syncthreads();
+    for (int64_t st = 0; st < nst; ++st) {
+      const int left = rows - st * kStage > kStage ? kStage : int(rows - st * kStage);
+      const int buf = int(st & 1);
+      const float2* pdu = du[buf];
+      const float *pb = bsm[buf] + q * SPL, *pc = csm[buf] + q * SPL;
+      float* py = ysm[buf];
+      constexpr int kGroup = 8;  // tokens unrolled
+#pragma unroll 1
+      for (int k0 = 0; k0 < left; k0 += kGroup) {
+        float p[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          const int k = k0 + i;
+          const float2 v = pdu[k * CH + place(k, ch)];
+          const float2 dd = dup(v.x), uu = dup(v.y);
+          float2 acc = dup(0.f);
+#pragma unroll
+          for (int m = 0; m < P; m += 2) {
+            const float4 bv = *reinterpret_cast<const float4*>(pb + k * NP + 2 * m);
+            const float2 l0 = mul2(dd, av[m]), l1 = mul2(dd, av[m + 1]);
+            h[m] =
+                fma2(make_float2(ex2(l0.x), ex2(l0.y)), h[m], mul2(uu, make_float2(bv.x, bv.y)));
+            h[m + 1] = fma2(make_float2(ex2(l1.x), ex2(l1.y)), h[m + 1],
+                            mul2(uu, make_float2(bv.z, bv.w)));
+            if (!SUMMARY) {
+              const float4 cv = *reinterpret_cast<const float4*>(pc + k * NP + 2 * m);
+              acc = m == 0 ? mul2(make_float2(cv.x, cv.y), h[0])
+                           : fma2(make_float2(cv.x, cv.y), h[m], acc);
+              acc = fma2(make_float2(cv.z, cv.w), h[m + 1], acc);
+            }
+          }
+          if (SUMMARY) sdt += v.x;
+          p[i] = acc.x + acc.y;
+        }
+        if (!SUMMARY) {
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) py[(k0 + i) * 32 + place(k0 + i, ch) * LPC + q] = p[i];
+        }
+      }
+      __syncthreads();
+    }
+    // the state after the unit
+    if (SUMMARY && con && q == 0) a.ws_dt[int64_t(unit) * a.dim + d] = sdt;
+    if (!con || (!SUMMARY && (!last || !a.state || (s0 == s1 && resume)))) return;
+    float* to = SUMMARY ? a.ws_state + (int64_t(unit) * a.dim + d) * N
+                        : a.state + (slot * a.dim + d) * N;
+#pragma unroll
+    for (int k = 0; k < SPL; ++k)
+      if (q * SPL + k < N) to[q * SPL + k] = k & 1 ? h[k / 2].y : h[k / 2].x;
+    return;
+  }
+
+  // the preparing warp: a lane's elements of a stage are rows row0 + i RX, channel (VEC:
+  // channels) c0 on
+  const bool gate = !SUMMARY && a.z;
   const int row0 = VEC ? lane / 2 : lane / CH, c0 = VEC ? lane % 2 * EX : lane % CH;
   const bool eon = c0 < nch;
   const int ec = d0 + (eon ? c0 : 0);
@@ -244,38 +314,53 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
   const T* pz = gate ? static_cast<const T*>(a.z) + t0 * a.zs + ec : nullptr;
   const T* pb = static_cast<const T*>(a.B) + t0 * a.bs + int64_t(g) * N;
   const T* pc = static_cast<const T*>(a.C) + t0 * a.cs + int64_t(g) * N;
-  float Dd[VEC ? EX : 1], bias[VEC ? EX : 1];
-#pragma unroll
-  for (int i = 0; i < (VEC ? EX : 1); ++i) {
-    Dd[i] = !SUMMARY && eon && a.D ? a.D[ec + i] : 0.f;
-    bias[i] = eon && a.dt_bias ? a.dt_bias[ec + i] : 0.f;
-  }
-  Raw<T, EX, VEC> rx, rz, zc;
-  Raw<TD, EX, VEC> rd;
-  Raw<T, EB, VEC> rb, rc;
-  // `left` rows from the stage at the pointers on; rows past them read the last one again
-  auto load = [&](int left) {
+  auto left_of = [&](int64_t st) {
+    return rows - st * kStage > kStage ? kStage : int(rows - st * kStage);
+  };
+  // A stage's values as loaded; two stages of them in flight where they come by wide loads
+  struct Loaded {
+    Raw<T, EX, VEC> x, z;
+    Raw<TD, EX, VEC> dt;
+    Raw<T, EB, VEC> b, c;
+  };
+  constexpr int kSets = VEC ? 2 : 1;
+  Loaded even, odd;
+  // D x and the gate of the two stages that are not finished
+  float skip0[EX], skip1[EX], gate0[EX], gate1[EX];
+  // rows kAhead stages on are asked into L2
+  auto ahead = [&](int64_t st) {
+    if ((st + kAhead + 1) * kStage > rows) return;  // the whole stage lies before the end
+    const int64_t r = kAhead * kStage + lane / 2;
+    prefetch_l2(px + r * a.xs);
+    prefetch_l2(pt + r * a.dts);
+    if (gate) prefetch_l2(pz + r * a.zs);
+    prefetch_l2(lane % 2 ? pb + r * a.bs : pc + r * a.cs);
+  };
+  auto load = [&](int64_t st, Loaded& r_) {  // rows past the end read the last one again
+    if (st >= nst) return;
+    const int left = left_of(st);
+    ahead(st);
     if constexpr (VEC) {
       const int64_t r = min(row0, left - 1);
-      rx.load(px + r * a.xs);
-      rd.load(pt + r * a.dts);
-      if (gate) rz.load(pz + r * a.zs);
-      rb.load(pb + r * a.bs + bn);
-      if (!SUMMARY) rc.load(pc + r * a.cs + bn);
+      r_.x.load(px + r * a.xs);
+      r_.dt.load(pt + r * a.dts);
+      if (gate) r_.z.load(pz + r * a.zs);
+      r_.b.load(pb + r * a.bs + bn);
+      if (!SUMMARY) r_.c.load(pc + r * a.cs + bn);
     } else {
 #pragma unroll
       for (int i = 0; i < EX; ++i) {
         const int64_t r = min(row0 + i * RX, left - 1);
-        rx.load1(i, px + r * a.xs);
-        rd.load1(i, pt + r * a.dts);
-        if (gate) rz.load1(i, pz + r * a.zs);
+        r_.x.load1(i, px + r * a.xs);
+        r_.dt.load1(i, pt + r * a.dts);
+        if (gate) r_.z.load1(i, pz + r * a.zs);
       }
 #pragma unroll
       for (int i = 0; i < EB; ++i) {
         const int64_t r = min(brow0 + i / CB * RB, left - 1);
         const int n = min(bn + i % CB * 32, N - 1);
-        rb.load1(i, pb + r * a.bs + n);
-        if (!SUMMARY) rc.load1(i, pc + r * a.cs + n);
+        r_.b.load1(i, pb + r * a.bs + n);
+        if (!SUMMARY) r_.c.load1(i, pc + r * a.cs + n);
       }
     }
     px += kStage * a.xs;
@@ -284,162 +369,138 @@ __global__ void __launch_bounds__(32) selective_varlen_kernel(const SelArgs a) {
     pb += kStage * a.bs;
     pc += kStage * a.cs;
   };
-
-  int64_t left64 = t1 - t0;
-  int left = left64 > kStage ? kStage : int(left64);  // rows of the current stage
-  if (left > 0) load(left);
-  int64_t yrow = t0 * a.ys;
-  for (; left64 > 0; left64 -= kStage) {
-    left = left64 > kStage ? kStage : int(left64);
-    float skip[EX];
+  float Dd[VEC ? EX : 1], bias[VEC ? EX : 1];
+  auto prepare = [&](int64_t st, const Loaded& r_) {
+    const int left = left_of(st), buf = int(st & 1);
+    constexpr int E2 = EX > 1 ? 2 : 1;
 #pragma unroll
-    for (int i = 0; i < EX; i += (EX > 1 ? 2 : 1)) {
-      float2 v2;
-      float xv[2], dv[2];
+    for (int i = 0; i < EX; i += E2) {
+      float xv[2] = {0.f, 0.f}, dv[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < (EX > 1 ? 2 : 1); ++e) {
-        xv[e] = rx.get(i + e);
-        dv[e] = rd.get(i + e) + bias[VEC ? i + e : 0];
-        skip[i + e] = Dd[VEC ? i + e : 0] * xv[e];
+      for (int e = 0; e < E2; ++e) {
+        xv[e] = r_.x.get(i + e);
+        dv[e] = r_.dt.get(i + e) + bias[VEC ? i + e : 0];
+        skip0[i + e] = skip1[i + e];
+        skip1[i + e] = Dd[VEC ? i + e : 0] * xv[e];
       }
-      if (EX == 1) dv[1] = xv[1] = 0.f;
-      v2 = make_float2(dv[0], dv[1]);
+      float2 v2 = make_float2(dv[0], dv[1]);
+      if (gate) {
+        const float2 zz = make_float2(r_.z.get(i), E2 > 1 ? r_.z.get(i + E2 - 1) : 0.f);
+        const float2 g2 = mul2(zz, sigmoid2(zz));
+        gate0[i] = gate1[i];
+        gate1[i] = g2.x;
+        if (E2 > 1) {
+          gate0[i + E2 - 1] = gate1[i + E2 - 1];
+          gate1[i + E2 - 1] = g2.y;
+        }
+      }
       if (a.softplus) v2 = softplus_acc2(v2);
 #pragma unroll
-      for (int e = 0; e < (EX > 1 ? 2 : 1); ++e) {
+      for (int e = 0; e < E2; ++e) {
         // rows past the end are identity steps
-        const bool on = eon && row0 + (i + e) * RX < left;
-        const float v = on ? (e ? v2.y : v2.x) : 0.f;
         const int k = row0 + (i + e) * RX;
-        du[k * CH + place(k, c0 + (VEC ? i + e : 0))] = make_float2(v, on ? v * xv[e] : 0.f);
+        const bool on = eon && k < left;
+        const float v = on ? (e ? v2.y : v2.x) : 0.f;
+        du[buf][k * CH + place(k, c0 + (VEC ? i + e : 0))] =
+            make_float2(v, on ? v * xv[e] : 0.f);
       }
     }
-    zc = rz;
     if constexpr (VEC) {
       const bool on = brow0 < left;
 #pragma unroll
       for (int i = 0; i < EB; i += 4) {
-        *reinterpret_cast<float4*>(bsm + lane * EB + i) =
-            on ? make_float4(rb.get(i), rb.get(i + 1), rb.get(i + 2), rb.get(i + 3))
+        *reinterpret_cast<float4*>(bsm[buf] + lane * EB + i) =
+            on ? make_float4(r_.b.get(i), r_.b.get(i + 1), r_.b.get(i + 2), r_.b.get(i + 3))
                : make_float4(0.f, 0.f, 0.f, 0.f);
         if (!SUMMARY)
-          *reinterpret_cast<float4*>(csm + lane * EB + i) =
-              on ? make_float4(rc.get(i), rc.get(i + 1), rc.get(i + 2), rc.get(i + 3))
+          *reinterpret_cast<float4*>(csm[buf] + lane * EB + i) =
+              on ? make_float4(r_.c.get(i), r_.c.get(i + 1), r_.c.get(i + 2), r_.c.get(i + 3))
                  : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < EB; ++i) {
         const bool on = bn + i % CB * 32 < N && brow0 + i / CB * RB < left;
-        bsm[i * 32 + lane] = on ? rb.get(i) : 0.f;
-        if (!SUMMARY) csm[i * 32 + lane] = on ? rc.get(i) : 0.f;
+        bsm[buf][i * 32 + lane] = on ? r_.b.get(i) : 0.f;
+        if (!SUMMARY) csm[buf][i * 32 + lane] = on ? r_.c.get(i) : 0.f;
       }
     }
-    __syncwarp();
-    if (left64 > kStage) load(left64 - kStage > kStage ? kStage : int(left64) - kStage);
-
-    // the steps, kGroup tokens unrolled
-    constexpr int kGroup = 8;
-#pragma unroll 1
-    for (int k0 = 0; k0 < left; k0 += kGroup) {
-      float p[kGroup];
+  };
+  auto finish = [&](int64_t st, const float (&skip)[EX], const float (&g)[EX]) {
+    const int left = left_of(st), buf = int(st & 1);
+    float v[EX];
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        const int k = k0 + i;
-        const float2 v = du[k * CH + place(k, ch)];
-        const float2 dd = dup(v.x), uu = dup(v.y);
-        float2 acc = dup(0.f);
+    for (int i = 0; i < EX; ++i) {
+      const int k = row0 + i * RX;
+      const float* pp = ysm[buf] + k * 32 + place(k, c0 + (VEC ? i : 0)) * LPC;
+      float sum = 0.f;
 #pragma unroll
-        for (int m = 0; m < P; m += 2) {
-          const float4 bv = *reinterpret_cast<const float4*>(bsm + k * NP + q * SPL + 2 * m);
-          const float2 l0 = mul2(dd, av[m]), l1 = mul2(dd, av[m + 1]);
-          h[m] = fma2(make_float2(ex2(l0.x), ex2(l0.y)), h[m], mul2(uu, make_float2(bv.x, bv.y)));
-          h[m + 1] = fma2(make_float2(ex2(l1.x), ex2(l1.y)), h[m + 1],
-                          mul2(uu, make_float2(bv.z, bv.w)));
-          if (!SUMMARY) {
-            const float4 cv = *reinterpret_cast<const float4*>(csm + k * NP + q * SPL + 2 * m);
-            acc = m == 0 ? mul2(make_float2(cv.x, cv.y), h[0])
-                         : fma2(make_float2(cv.x, cv.y), h[m], acc);
-            acc = fma2(make_float2(cv.z, cv.w), h[m + 1], acc);
-          }
+      for (int e = 0; e < LPC; e += LPC < 4 ? LPC : 4) {
+        if constexpr (LPC == 2) {
+          const float2 f = *reinterpret_cast<const float2*>(pp);
+          sum = f.x + f.y;
+        } else {
+          const float4 f = *reinterpret_cast<const float4*>(pp + e);
+          sum += (f.x + f.y) + (f.z + f.w);
         }
-        if (SUMMARY) sdt += v.x;
-        p[i] = acc.x + acc.y;
       }
-      if (!SUMMARY) {
-        // the lanes' sums meet in shared memory, added when the stage's y is finished
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) ysm[(k0 + i) * 32 + place(k0 + i, ch) * LPC + q] = p[i];
-      }
+      v[i] = skip[i] + sum;
+      if (gate) v[i] *= g[i];
     }
-    __syncwarp();
-    if (!SUMMARY) {
-      float v[EX];
+    const int64_t yrow = (t0 + st * kStage) * a.ys;
+    if constexpr (VEC) {
+      if (eon && row0 < left) {
+        const int64_t to = yrow + row0 * a.ys + ec;
+        if (a.y_bf16) {
+          uint32_t w[EX / 2];
+#pragma unroll
+          for (int i = 0; i < EX; i += 2) w[i / 2] = pack_bf16x2(v[i], v[i + 1]);
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.y) + to;
+          if constexpr (EX == 8) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+          else *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < EX; i += 4)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + to + i) =
+                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < EX; ++i) {
-        const int k = row0 + i * RX;
-        const float* pp = ysm + k * 32 + place(k, c0 + (VEC ? i : 0)) * LPC;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < LPC; e += LPC < 4 ? LPC : 4) {
-          if constexpr (LPC == 2) {
-            const float2 f = *reinterpret_cast<const float2*>(pp);
-            sum = f.x + f.y;
-          } else {
-            const float4 f = *reinterpret_cast<const float4*>(pp + e);
-            sum += (f.x + f.y) + (f.z + f.w);
-          }
-        }
-        v[i] = skip[i] + sum;
+        if (!eon || row0 + i * RX >= left) continue;
+        const int64_t to = yrow + (row0 + i * RX) * a.ys + ec;
+        if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v[i]);
+        else static_cast<float*>(a.y)[to] = v[i];
       }
-      if (gate) {
-#pragma unroll
-        for (int i = 0; i < EX; i += (EX > 1 ? 2 : 1)) {
-          const float2 zz = make_float2(zc.get(i), EX > 1 ? zc.get(i + (EX > 1)) : 0.f);
-          const float2 g2 = mul2(zz, sigmoid2(zz));
-          v[i] *= g2.x;
-          if (EX > 1) v[i + (EX > 1)] *= g2.y;
-        }
-      }
-      if constexpr (VEC) {
-        if (eon && row0 < left) {
-          const int64_t to = yrow + row0 * a.ys + ec;
-          if (a.y_bf16) {
-            uint32_t w[EX / 2];
-#pragma unroll
-            for (int i = 0; i < EX; i += 2) w[i / 2] = pack_bf16x2(v[i], v[i + 1]);
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.y) + to;
-            if constexpr (EX == 8)
-              *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-            else *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < EX; i += 4)
-              *reinterpret_cast<float4*>(static_cast<float*>(a.y) + to + i) =
-                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < EX; ++i) {
-          if (!eon || row0 + i * RX >= left) continue;
-          const int64_t to = yrow + (row0 + i * RX) * a.ys + ec;
-          if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v[i]);
-          else static_cast<float*>(a.y)[to] = v[i];
-        }
-      }
-      yrow += kStage * a.ys;
     }
-  }
+  };
 
-  // the state after the unit
-  if (SUMMARY && con && q == 0) a.ws_dt[int64_t(unit) * a.dim + d] = sdt;
-  if (!con || (!SUMMARY && (!last || !a.state || (s0 == s1 && resume)))) return;
-  float* to = SUMMARY ? a.ws_state + (int64_t(unit) * a.dim + d) * N
-                      : a.state + (slot * a.dim + d) * N;
+  load(0, even);
+  if (kSets == 2) load(1, odd);
 #pragma unroll
-  for (int k = 0; k < SPL; ++k)
-    if (q * SPL + k < N) to[q * SPL + k] = k & 1 ? h[k / 2].y : h[k / 2].x;
+  for (int i = 0; i < (VEC ? EX : 1); ++i) {
+    Dd[i] = !SUMMARY && eon && a.D ? a.D[ec + i] : 0.f;
+    bias[i] = eon && a.dt_bias ? a.dt_bias[ec + i] : 0.f;
+  }
+  if (nst > 0) prepare(0, even);
+  load(kSets, even);
+  __syncthreads();
+  auto round = [&](int64_t st, Loaded& next) {  // the other warp is on stage st
+    if (!SUMMARY && st > 0) finish(st - 1, skip0, gate0);
+    if (st + 1 < nst) prepare(st + 1, next);
+    load(st + 1 + kSets, next);
+    __syncthreads();
+  };
+  if constexpr (kSets == 2) {
+    for (int64_t st = 0; st < nst; st += 2) {
+      round(st, odd);
+      if (st + 1 < nst) round(st + 1, even);
+    }
+  } else {
+    for (int64_t st = 0; st < nst; ++st) round(st, even);
+  }
+  if (!SUMMARY && nst > 0) finish(nst - 1, skip1, gate1);
 }
 
 // One token of each sequence.  LPC lanes per channel with 4 states each, a warp on 32 / LPC
