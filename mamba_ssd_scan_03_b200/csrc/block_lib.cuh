@@ -238,11 +238,14 @@ ssd::cache::SelArgs sel_args(const ssd_selective_args* a) {
 }
 
 template <typename T, typename TD, int LPC, int SPL, bool VEC>
-ssd_status launch_sel(const ssd::cache::SelArgs& k, const SelPlan& p, cudaStream_t stream) {
+ssd_status launch_sel(ssd::cache::SelArgs k, const SelPlan& p, cudaStream_t stream) {
   namespace cc = ssd::cache;
   const int64_t ncb = sel_blocks(k.dim, k.ngroups, LPC);
   if (p.units * ncb > INT32_MAX) return SSD_ERR_UNSUPPORTED;
   const unsigned grid = unsigned(p.units * ncb);
+  // more CTAs than the GPU holds at a time (eight to an SM): the longest sequences first, so that
+  // none of them starts last
+  k.by_length = !k.chunk && k.nseq > 1 && k.nseq <= cc::kSorted && grid > 8u * sm_count();
   if (k.chunk) {
     cc::selective_varlen_kernel<T, TD, LPC, SPL, VEC, true><<<grid, 64, 0, stream>>>(k);
     const ssd_status st = launched();

@@ -13,6 +13,8 @@
 // Every (token, channel, state) needs its own exponential: dstate ex2 per token and channel at
 // 16 per clock and SM bound the prompts' kernel; the token kernel streams the states.
 #pragma once
+#include <limits.h>
+
 #include "conv_cache_kernels.cuh"
 
 namespace ssd {
@@ -40,6 +42,7 @@ struct SelArgs {
   int chunk;   // tokens per unit (0: a unit is a whole sequence)
   int nunits;  // units the workspace has room for: ntok / chunk + nseq
   bool io_bf16, dt_bf16, y_bf16, softplus;
+  bool by_length;  // whole sequences only, at most kSorted: the longest come first
 };
 
 // Decay rates in log2 units; a rate of -inf is held finite, so that an identity step (dt = 0)
@@ -125,12 +128,43 @@ struct Raw {
 // C anew; with four lanes of four states that takes longer than the exponentials.
 constexpr int kStage = 16, kAhead = 2;
 
+// The sequence that `rank` others come before, by falling length; nseq <= kSorted.  Call with the
+// whole warp.
+constexpr int kSorted = 128;
+__device__ __forceinline__ int seq_of_rank(const int* __restrict__ cu, int nseq, int rank) {
+  constexpr int M = kSorted / 32;
+  const int lane = threadIdx.x & 31;
+  int len[M], before[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int i = m * 32 + lane;
+    len[m] = i < nseq ? cu[i + 1] - cu[i] : INT_MIN;
+    before[m] = 0;
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll 1
+    for (int e = 0; e < 32 && m * 32 + e < nseq; ++e) {
+      const int l = __shfl_sync(0xffffffffu, len[m], e), j = m * 32 + e;
+#pragma unroll
+      for (int k = 0; k < M; ++k)
+        before[k] += l > len[k] || (l == len[k] && j < k * 32 + lane);
+    }
+  int found = 0;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const unsigned hit = __ballot_sync(0xffffffffu, m * 32 + lane < nseq && before[m] == rank);
+    if (hit) found = m * 32 + __ffs(hit) - 1;
+  }
+  return found;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 template <typename T, typename TD, int LPC, int SPL, bool VEC, bool SUMMARY>
-__global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
+__global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a) {
   constexpr int CH = 32 / LPC;         // channels of the unit
   constexpr int NP = LPC * SPL;        // states, padded
   constexpr int EX = CH / 2;           // x, dt, z elements per lane and stage
@@ -172,7 +206,8 @@ __global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
   if (!SUMMARY && blockIdx.x == 0) warp_check_seqs(a.cu, a.nseq, a.ntok);
 
   // the unit's sequence, and its chunk within the sequence
-  int seq = unit, chunk = 0, nchunk = 1;
+  int seq = !a.chunk && a.by_length ? seq_of_rank(a.cu, a.nseq, unit) : unit;
+  int chunk = 0, nchunk = 1;
   if (a.chunk) {
     seq = -1;
     int base = 0;
@@ -317,14 +352,9 @@ __global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
   auto left_of = [&](int64_t st) {
     return rows - st * kStage > kStage ? kStage : int(rows - st * kStage);
   };
-  // A stage's values as loaded; two stages of them in flight where they come by wide loads
-  struct Loaded {
-    Raw<T, EX, VEC> x, z;
-    Raw<TD, EX, VEC> dt;
-    Raw<T, EB, VEC> b, c;
-  };
-  constexpr int kSets = VEC ? 2 : 1;
-  Loaded even, odd;
+  Raw<T, EX, VEC> rx, rz;
+  Raw<TD, EX, VEC> rd;
+  Raw<T, EB, VEC> rb, rc;
   // D x and the gate of the two stages that are not finished
   float skip0[EX], skip1[EX], gate0[EX], gate1[EX];
   // rows kAhead stages on are asked into L2
@@ -336,31 +366,31 @@ __global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
     if (gate) prefetch_l2(pz + r * a.zs);
     prefetch_l2(lane % 2 ? pb + r * a.bs : pc + r * a.cs);
   };
-  auto load = [&](int64_t st, Loaded& r_) {  // rows past the end read the last one again
+  auto load = [&](int64_t st) {  // rows past the end read the last one again
     if (st >= nst) return;
     const int left = left_of(st);
     ahead(st);
     if constexpr (VEC) {
       const int64_t r = min(row0, left - 1);
-      r_.x.load(px + r * a.xs);
-      r_.dt.load(pt + r * a.dts);
-      if (gate) r_.z.load(pz + r * a.zs);
-      r_.b.load(pb + r * a.bs + bn);
-      if (!SUMMARY) r_.c.load(pc + r * a.cs + bn);
+      rx.load(px + r * a.xs);
+      rd.load(pt + r * a.dts);
+      if (gate) rz.load(pz + r * a.zs);
+      rb.load(pb + r * a.bs + bn);
+      if (!SUMMARY) rc.load(pc + r * a.cs + bn);
     } else {
 #pragma unroll
       for (int i = 0; i < EX; ++i) {
         const int64_t r = min(row0 + i * RX, left - 1);
-        r_.x.load1(i, px + r * a.xs);
-        r_.dt.load1(i, pt + r * a.dts);
-        if (gate) r_.z.load1(i, pz + r * a.zs);
+        rx.load1(i, px + r * a.xs);
+        rd.load1(i, pt + r * a.dts);
+        if (gate) rz.load1(i, pz + r * a.zs);
       }
 #pragma unroll
       for (int i = 0; i < EB; ++i) {
         const int64_t r = min(brow0 + i / CB * RB, left - 1);
         const int n = min(bn + i % CB * 32, N - 1);
-        r_.b.load1(i, pb + r * a.bs + n);
-        if (!SUMMARY) r_.c.load1(i, pc + r * a.cs + n);
+        rb.load1(i, pb + r * a.bs + n);
+        if (!SUMMARY) rc.load1(i, pc + r * a.cs + n);
       }
     }
     px += kStage * a.xs;
@@ -370,7 +400,7 @@ __global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
     pc += kStage * a.cs;
   };
   float Dd[VEC ? EX : 1], bias[VEC ? EX : 1];
-  auto prepare = [&](int64_t st, const Loaded& r_) {
+  auto prepare = [&](int64_t st) {
     const int left = left_of(st), buf = int(st & 1);
     constexpr int E2 = EX > 1 ? 2 : 1;
 #pragma unroll
@@ -378,14 +408,14 @@ __global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
       float xv[2] = {0.f, 0.f}, dv[2] = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < E2; ++e) {
-        xv[e] = r_.x.get(i + e);
-        dv[e] = r_.dt.get(i + e) + bias[VEC ? i + e : 0];
+        xv[e] = rx.get(i + e);
+        dv[e] = rd.get(i + e) + bias[VEC ? i + e : 0];
         skip0[i + e] = skip1[i + e];
         skip1[i + e] = Dd[VEC ? i + e : 0] * xv[e];
       }
       float2 v2 = make_float2(dv[0], dv[1]);
       if (gate) {
-        const float2 zz = make_float2(r_.z.get(i), E2 > 1 ? r_.z.get(i + E2 - 1) : 0.f);
+        const float2 zz = make_float2(rz.get(i), E2 > 1 ? rz.get(i + E2 - 1) : 0.f);
         const float2 g2 = mul2(zz, sigmoid2(zz));
         gate0[i] = gate1[i];
         gate1[i] = g2.x;
@@ -410,19 +440,19 @@ __global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
 #pragma unroll
       for (int i = 0; i < EB; i += 4) {
         *reinterpret_cast<float4*>(bsm[buf] + lane * EB + i) =
-            on ? make_float4(r_.b.get(i), r_.b.get(i + 1), r_.b.get(i + 2), r_.b.get(i + 3))
+            on ? make_float4(rb.get(i), rb.get(i + 1), rb.get(i + 2), rb.get(i + 3))
                : make_float4(0.f, 0.f, 0.f, 0.f);
         if (!SUMMARY)
           *reinterpret_cast<float4*>(csm[buf] + lane * EB + i) =
-              on ? make_float4(r_.c.get(i), r_.c.get(i + 1), r_.c.get(i + 2), r_.c.get(i + 3))
+              on ? make_float4(rc.get(i), rc.get(i + 1), rc.get(i + 2), rc.get(i + 3))
                  : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < EB; ++i) {
         const bool on = bn + i % CB * 32 < N && brow0 + i / CB * RB < left;
-        bsm[buf][i * 32 + lane] = on ? r_.b.get(i) : 0.f;
-        if (!SUMMARY) csm[buf][i * 32 + lane] = on ? r_.c.get(i) : 0.f;
+        bsm[buf][i * 32 + lane] = on ? rb.get(i) : 0.f;
+        if (!SUMMARY) csm[buf][i * 32 + lane] = on ? rc.get(i) : 0.f;
       }
     }
   };
@@ -476,29 +506,20 @@ __global__ void __launch_bounds__(64) selective_varlen_kernel(const SelArgs a) {
     }
   };
 
-  load(0, even);
-  if (kSets == 2) load(1, odd);
+  load(0);
 #pragma unroll
   for (int i = 0; i < (VEC ? EX : 1); ++i) {
     Dd[i] = !SUMMARY && eon && a.D ? a.D[ec + i] : 0.f;
     bias[i] = eon && a.dt_bias ? a.dt_bias[ec + i] : 0.f;
   }
-  if (nst > 0) prepare(0, even);
-  load(kSets, even);
+  if (nst > 0) prepare(0);
+  load(1);
   __syncthreads();
-  auto round = [&](int64_t st, Loaded& next) {  // the other warp is on stage st
+  for (int64_t st = 0; st < nst; ++st) {  // the other warp is on stage st
     if (!SUMMARY && st > 0) finish(st - 1, skip0, gate0);
-    if (st + 1 < nst) prepare(st + 1, next);
-    load(st + 1 + kSets, next);
+    if (st + 1 < nst) prepare(st + 1);
+    load(st + 2);
     __syncthreads();
-  };
-  if constexpr (kSets == 2) {
-    for (int64_t st = 0; st < nst; st += 2) {
-      round(st, odd);
-      if (st + 1 < nst) round(st + 1, even);
-    }
-  } else {
-    for (int64_t st = 0; st < nst; ++st) round(st, even);
   }
   if (!SUMMARY && nst > 0) finish(nst - 1, skip1, gate1);
 }
