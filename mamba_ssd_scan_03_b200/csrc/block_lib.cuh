@@ -62,7 +62,7 @@ template <typename T, int K, int VW>
 void launch_conv(const ssd::cache::ConvArgs<T>& a, cudaStream_t stream) {
   const int64_t runs = std::max<int64_t>(1, (a.ntok + a.run - 1) / a.run);
   const int64_t ncb = (a.cdim + 32 * VW - 1) / (32 * VW);
-  ssd::cache::conv_varlen_kernel<T, K, VW, VW == 1 ? 16 : 8>
+  ssd::cache::conv_varlen_kernel<T, K, VW, VW == 1 ? 8 : 6>
       <<<unsigned(runs * ncb), 32, 0, stream>>>(a);
 }
 template <typename T, int K, int VW>
@@ -174,8 +174,10 @@ SelPlan make_sel_plan(int64_t ntok, int nseq, int dim, int dstate, int ngroups, 
   p.chunk = 0;
   p.units = nseq;
   if (warps < sched && len >= 128) {
-    // four warps per scheduler, chunks of at least 64 tokens
-    const int64_t want = std::min((4 * sched + warps - 1) / warps, len / 64);
+    // two full rounds of CTAs (eight to an SM), chunks of at least 64 tokens.  One prompt of 16384
+    // tokens and 1536 channels: 301 us, 366 with half as many chunks, 342 with three times as many,
+    // 1020 uncut; of 8192 and 5120: 486, 614, 484
+    const int64_t want = std::min(4 * sched / warps, len / 64);
     if (want > 2) {
       p.chunk = int((len + want - 1) / want + 15) / 16 * 16;
       p.units = ntok / p.chunk + nseq;

@@ -121,6 +121,37 @@ __device__ __forceinline__ void conv_silu_row(const float (&win)[W][VW], int fir
   }
 }
 
+// NV neighbouring values of a row as they lie in memory (one or two wide accesses), or one value
+// per word.  Loading and converting are kept apart, and nothing branches between a load and the
+// stage that converts it: a value is first waited for there.
+template <typename T, int NV, bool VEC>
+struct Raw {
+  static constexpr int kWords = VEC ? NV * int(sizeof(T)) / 4 : NV;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {  // VEC
+    const unsigned char* q = reinterpret_cast<const unsigned char*>(p);
+    if constexpr (kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kWords / 4; ++k) {
+        const uint4 v = reinterpret_cast<const uint4*>(q)[k];
+        w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void load1(int i, const T* p) {  // one value per word
+    if constexpr (sizeof(T) == 2) w[i] = *reinterpret_cast<const unsigned short*>(p);
+    else w[i] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (VEC) return (i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+    else return bf16lo(w[i]);
+  }
+};
+
 // A warp's answer: the slot of sequence i, or -1 where the sequence is to be left alone: a
 // negative slot (padding), one past the cache, or one that an earlier sequence of the call
 // names too (the last two are latched as SSD_ERR_INDEX).  Call with the whole warp.
@@ -306,15 +337,24 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) load_ch<T, VW>(ub + (b - (K - 1) + k) * a.us, win[k]);
       }
-      for (int64_t t = b; t < end; t += STEP) {
+      // a step's rows as loaded: the next step's are on their way while this one's are worked on;
+      // rows past the end read the last one again, and are not written
+      Raw<T, VW, VW == 4> raw[STEP];
+      auto load = [&](int64_t t) {
 #pragma unroll
         for (int i = 0; i < STEP; ++i) {
-          if (t + i < end) load_ch<T, VW>(ub + (t + i) * a.us, win[K - 1 + i]);
-          else {
-#pragma unroll
-            for (int j = 0; j < VW; ++j) win[K - 1 + i][j] = 0.f;
-          }
+          const T* p = ub + (t + i < end ? t + i : end - 1) * a.us;
+          if constexpr (VW == 4) raw[i].load(p);
+          else raw[i].load1(0, p);
         }
+      };
+      load(b);
+      for (int64_t t = b; t < end; t += STEP) {
+#pragma unroll
+        for (int i = 0; i < STEP; ++i)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) win[K - 1 + i][j] = raw[i].get(j);
+        if (t + STEP < end) load(t + STEP);
 #pragma unroll
         for (int i = 0; i < STEP; ++i) {
           if (t + i < end) {

@@ -137,6 +137,63 @@ constexpr int kDepth = 3;  // at most; fewer where a CTA's rows are too long (No
 __host__ __device__ inline int ring_vecs(const NormArgs& a) {  // 16-byte pieces of 8 channels
   return (a.y_bf16 ? 1 : 2) + (a.z ? (a.z_bf16 ? 1 : 2) : 0) + (a.dout ? (a.o_bf16 ? 1 : 2) : 0);
 }
+// Where a thread's copies of its next row come from, one running pointer per input.  The forward
+// kernel keeps them (143 -> 136 us at 16384 x 5120); the backward one finds the addresses anew for
+// each row, as its registers are scarce (held there, they spill others: 266 -> 301 us).
+template <int NV>
+struct Ahead {
+  const char *y, *z, *d;
+  int64_t ys, zs, ds;  // bytes to the thread's next row
+  int yu, zu, du;      // bytes between its units
+  template <typename Pl>
+  __device__ __forceinline__ Ahead(const NormArgs& a, const Pl& p, int c0) {
+    const int c = c0 + p.col(0), lanes = p.lanes * 8;
+    auto at = [&](const void* base, int64_t stride, bool bf16, const char*& ptr, int64_t& step,
+                  int& unit) {
+      const int es = bf16 ? 2 : 4;
+      ptr = static_cast<const char*>(base) + (p.row * stride + c) * es;
+      step = p.step * stride * es;
+      unit = lanes * es;
+    };
+    at(a.y, a.ys, a.y_bf16, y, ys, yu);
+    if (a.z) at(a.z, a.zs, a.z_bf16, z, zs, zu);
+    if (a.dout) at(a.dout, a.os, a.o_bf16, d, ds, du);
+  }
+  __device__ __forceinline__ void next(const NormArgs& a) {
+    y += ys;
+    if (a.z) z += zs;
+    if (a.dout) d += ds;
+  }
+};
+__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <int LANES, int NV, int VW>
+__device__ __forceinline__ void norm_fill(const NormArgs& a, const Place<LANES, NV, VW>& p,
+                                          const Ahead<NV>& from, int64_t row, uint4* ring) {
+  if constexpr (VW == 8) {
+    if (p.on && row < a.rows) {
+      uint32_t to = uint32_t(__cvta_generic_to_shared(ring));
+      const uint32_t piece = blockDim.x * 16;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = p.col(i) < p.gs;
+        auto copy = [&](const char* src, bool bf16) {
+          if (in) copy16(to, src);
+          to += piece;
+          if (!bf16) {
+            if (in) copy16(to, src + 16);
+            to += piece;
+          }
+        };
+        copy(from.y + i * from.yu, a.y_bf16);
+        if (a.z) copy(from.z + i * from.zu, a.z_bf16);
+        if (a.dout) copy(from.d + i * from.du, a.o_bf16);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+}
 template <int LANES, int NV, int VW>
 __device__ __forceinline__ void norm_fill(const NormArgs& a, const Place<LANES, NV, VW>& p, int c0,
                                           int64_t row, uint4* ring) {
@@ -148,12 +205,9 @@ __device__ __forceinline__ void norm_fill(const NormArgs& a, const Place<LANES, 
         if (c >= p.gs) continue;
         uint4* to = ring + i * ring_vecs(a) * blockDim.x;
         auto copy = [&](const void* base, int64_t at, bool bf16) {
-          const char* from = static_cast<const char*>(base) + at * (bf16 ? 2 : 4);
+          const char* src = static_cast<const char*>(base) + at * (bf16 ? 2 : 4);
           for (int k = 0; k < (bf16 ? 1 : 2); ++k, to += blockDim.x)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             uint32_t(__cvta_generic_to_shared(to))),
-                         "l"(from + 16 * k)
-                         : "memory");
+            copy16(uint32_t(__cvta_generic_to_shared(to)), src + 16 * k);
         };
         copy(a.y, row * a.ys + c0 + c, a.y_bf16);
         if (a.z) copy(a.z, row * a.zs + c0 + c, a.z_bf16);
@@ -216,18 +270,28 @@ __device__ __forceinline__ void put(float (&v)[VW], int j, float2 f) {
 }
 
 // The rows of a CTA: row(k) is handed on with its ring stage when its copies have landed.
-template <int LANES, int NV, int VW, typename F>
+template <bool KEEP, int LANES, int NV, int VW, typename F>
 __device__ __forceinline__ void norm_rows(const NormArgs& a, const Place<LANES, NV, VW>& p, int c0,
                                           uint4* ring, const F& each) {
   const int per = VW == 8 ? NV * ring_vecs(a) * int(blockDim.x) : 0;  // of a stage
   ring += threadIdx.x;
   int in = 0, par = 0;
   int64_t ahead = p.row;
-  for (; in < a.depth - 1; ++in, ahead += p.step) norm_fill(a, p, c0, ahead, ring + in * per);
+  Ahead<NV> from(a, p, c0);
+  auto fill = [&] {
+    if constexpr (KEEP) {
+      norm_fill(a, p, from, ahead, ring + in * per);
+      from.next(a);
+    } else {
+      norm_fill(a, p, c0, ahead, ring + in * per);
+    }
+    ahead += p.step;
+  };
+  for (; in < a.depth - 1; ++in) fill();
   int at = 0;
   // every team of a CTA runs the same number of rounds: the sums are collective
-  for (int64_t r0 = 0; r0 < a.rows; r0 += p.step, ahead += p.step, par ^= 1) {
-    norm_fill(a, p, c0, ahead, ring + in * per);
+  for (int64_t r0 = 0; r0 < a.rows; r0 += p.step, par ^= 1) {
+    fill();
     in = in + 1 == a.depth ? 0 : in + 1;
     if constexpr (VW == 8) {  // all but the depth - 1 youngest rows have landed
       if (a.depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
@@ -256,7 +320,7 @@ __global__ void __launch_bounds__(MAXT, MINB) group_norm_kernel(const NormArgs a
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (p.on && p.col(i) < p.gs) load_n<VW>(a.w, c0 + p.col(i), false, w[i]);
-  norm_rows(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
+  norm_rows<true>(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
     const bool live = p.on && row < a.rows;
     float v[NV][VW];
     float2 s2 = dup(0.f);
@@ -351,7 +415,7 @@ __global__ void __launch_bounds__(MAXT, MINB) group_norm_bwd_kernel(const NormAr
   }
   const float inv = 1.f / p.gs;
   const bool first = a.z && a.gate_first, last = a.z && !a.gate_first;
-  norm_rows(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
+  norm_rows<false>(a, p, c0, ring, [&](int64_t row, const uint4* st, int par) {
     const bool live = p.on && row < a.rows;
     // v and do of a unit's pair j, as both passes need them
     float y[VW], z[VW], d[VW];

@@ -68,46 +68,6 @@ __device__ __forceinline__ float softplus_acc(float v) {
   for (int k = 8; k >= 0; --k) p = fmaf(p, e, log1p_coef(k));
   return fmaf(p, e, fmaxf(v, 0.f));
 }
-// The same of a pair.
-__device__ __forceinline__ float2 softplus_acc2(float2 v) {
-  const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
-  float2 p = dup(log1p_coef(9));
-#pragma unroll
-  for (int k = 8; k >= 0; --k) p = fma2(p, e, dup(log1p_coef(k)));
-  return fma2(p, e, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
-}
-
-// NV neighbouring values of a row as they lie in memory (one or two wide accesses), or one value
-// per word.  Loading and converting are kept apart, and nothing branches between a load and the
-// stage that converts it: a value is first waited for there.
-template <typename T, int NV, bool VEC>
-struct Raw {
-  static constexpr int kWords = VEC ? NV * int(sizeof(T)) / 4 : NV;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void load(const T* p) {  // VEC
-    const unsigned char* q = reinterpret_cast<const unsigned char*>(p);
-    if constexpr (kWords == 2) {
-      const uint2 v = *reinterpret_cast<const uint2*>(q);
-      w[0] = v.x; w[1] = v.y;
-    } else {
-#pragma unroll
-      for (int k = 0; k < kWords / 4; ++k) {
-        const uint4 v = reinterpret_cast<const uint4*>(q)[k];
-        w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
-      }
-    }
-  }
-  __device__ __forceinline__ void load1(int i, const T* p) {  // one value per word
-    if constexpr (sizeof(T) == 2) w[i] = *reinterpret_cast<const unsigned short*>(p);
-    else w[i] = *reinterpret_cast<const uint32_t*>(p);
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    else if constexpr (VEC) return (i & 1) ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
-    else return bf16lo(w[i]);
-  }
-};
-
 // Two warps scan one unit: a sequence (chunk == 0) or a chunk of one, for 32 / LPC channels of
 // one group; LPC lanes per channel hold SPL of its states each.  SUMMARY: only the state after
 // the chunk, from zero (or, for a sequence's first chunk, from the sequence's initial state), and
@@ -126,7 +86,7 @@ struct Raw {
 // Why two lanes per channel for 16 states: reading B and C fills registers at 128 bytes a clock
 // and SM, or 256 where a warp reads one or two addresses, and every lane reads its states' B and
 // C anew; with four lanes of four states that takes longer than the exponentials.
-constexpr int kStage = 16, kAhead = 2;
+constexpr int kStage = 16;
 
 // The sequence that `rank` others come before, by falling length; nseq <= kSorted.  Call with the
 // whole warp.
@@ -157,10 +117,6 @@ __device__ __forceinline__ int seq_of_rank(const int* __restrict__ cu, int nseq,
     if (hit) found = m * 32 + __ffs(hit) - 1;
   }
   return found;
-}
-
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 template <typename T, typename TD, int LPC, int SPL, bool VEC, bool SUMMARY>
@@ -255,32 +211,43 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
     const int q = lane % LPC, ch = lane / LPC;
     const bool con = ch < nch;
     const int d = d0 + (con ? ch : 0);
-    float2 av[P], h[P];
+    float rate[SPL], hv[SPL];
+    const float* from = nullptr;  // the state that the chunk starts from, or its first part
+    if (resume && chunk == 0 && (SUMMARY || nchunk == 1)) from = a.state + (slot * a.dim + d) * N;
+    // a sequence cut into chunks: its initial state was copied by the summary launch (the last
+    // chunk may already have moved the slot's), the others' follow from the summaries
+    const int64_t u0 = unit - chunk;
+    auto summary = [&](int64_t u) { return a.ws_state + (u * a.dim + d) * N; };
+    if (!SUMMARY && nchunk > 1 && (chunk > 0 || resume))
+      from = summary(chunk > 0 ? u0 : u0 + nchunk - 1);
 #pragma unroll
     for (int k = 0; k < SPL; ++k) {
       const int n = q * SPL + k;
-      const bool on = con && n < N;
-      const float rate = on ? rate2(a.A[int64_t(d) * N + n]) : 0.f;
-      float hv = 0.f;
-      if (on && resume && chunk == 0 && (SUMMARY || nchunk == 1))
-        hv = a.state[(slot * a.dim + d) * N + n];
-      if (on && !SUMMARY && nchunk > 1) {
-        // a sequence cut into chunks: its initial state was copied by the summary launch (the
-        // last chunk may already have moved the slot's), the others' follow from the summaries
-        const int64_t u0 = unit - chunk;
-        if (chunk == 0) {
-          if (resume) hv = a.ws_state[((u0 + nchunk - 1) * a.dim + d) * N + n];
-        } else {
-          hv = a.ws_state[(u0 * a.dim + d) * N + n];
-          for (int j = 1; j < chunk; ++j)
-            hv = fmaf(ex2(rate * a.ws_dt[(u0 + j) * a.dim + d]), hv,
-                      a.ws_state[((u0 + j) * a.dim + d) * N + n]);
+      rate[k] = n < N ? rate2(a.A[int64_t(d) * N + n]) : 0.f;
+      hv[k] = from && n < N ? from[n] : 0.f;
+    }
+    if (!SUMMARY && nchunk > 1) {
+#pragma unroll 2
+      for (int j = 1; j < chunk; ++j) {
+        const float sum = a.ws_dt[(u0 + j) * a.dim + d];
+        const float* p = summary(u0 + j);
+#pragma unroll
+        for (int k = 0; k < SPL; ++k) {
+          const int n = q * SPL + k;
+          hv[k] = fmaf(ex2(rate[k] * sum), hv[k], n < N ? p[n] : 0.f);
         }
       }
-      if (on && SUMMARY && chunk == 0 && resume)
-        a.ws_state[(int64_t(unit + nchunk - 1) * a.dim + d) * N + n] = hv;
-      (k & 1 ? av[k / 2].y : av[k / 2].x) = rate;
-      (k & 1 ? h[k / 2].y : h[k / 2].x) = hv;
+    }
+    if (SUMMARY && chunk == 0 && resume && con) {
+#pragma unroll
+      for (int k = 0; k < SPL; ++k)
+        if (q * SPL + k < N) summary(unit + nchunk - 1)[q * SPL + k] = hv[k];
+    }
+    float2 av[P], h[P];
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+      av[m] = make_float2(rate[2 * m], rate[2 * m + 1]);
+      h[m] = make_float2(hv[2 * m], hv[2 * m + 1]);
     }
     float sdt = 0.f;
     __syncthreads();
@@ -357,19 +324,9 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
   Raw<T, EB, VEC> rb, rc;
   // D x and the gate of the two stages that are not finished
   float skip0[EX], skip1[EX], gate0[EX], gate1[EX];
-  // rows kAhead stages on are asked into L2
-  auto ahead = [&](int64_t st) {
-    if ((st + kAhead + 1) * kStage > rows) return;  // the whole stage lies before the end
-    const int64_t r = kAhead * kStage + lane / 2;
-    prefetch_l2(px + r * a.xs);
-    prefetch_l2(pt + r * a.dts);
-    if (gate) prefetch_l2(pz + r * a.zs);
-    prefetch_l2(lane % 2 ? pb + r * a.bs : pc + r * a.cs);
-  };
   auto load = [&](int64_t st) {  // rows past the end read the last one again
     if (st >= nst) return;
     const int left = left_of(st);
-    ahead(st);
     if constexpr (VEC) {
       const int64_t r = min(row0, left - 1);
       rx.load(px + r * a.xs);
@@ -424,7 +381,7 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
           gate1[i + E2 - 1] = g2.y;
         }
       }
-      if (a.softplus) v2 = softplus_acc2(v2);
+      if (a.softplus) v2 = make_float2(softplus_acc(v2.x), softplus_acc(v2.y));
 #pragma unroll
       for (int e = 0; e < E2; ++e) {
         // rows past the end are identity steps
