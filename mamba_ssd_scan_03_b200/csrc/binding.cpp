@@ -194,6 +194,9 @@ PyObject* conv(PyObject* ou, PyObject* ow, PyObject* ocu, PyObject* obias, PyObj
     state = whole(ostate, "conv_state", u.scalar_type(), {t.size(0), K - 1, C}, dev);
     if (K > 1) nslots = t.size(0);
     else state = nullptr;
+    // a cache without a slot is not the same as none (its address is NULL, too)
+    if (K > 1 && nslots == 0 && (step ? rows : s.nseq) > 0)
+      return PyLong_FromLong(SSD_ERR_INVALID_ARG);
   }
   const float* pw = weights(ow, "w", {C, K}, dev);
   const float* bias = whole<float>(obias, "bias", at::kFloat, {C}, dev);
@@ -227,6 +230,7 @@ struct Selective {
   at::Tensor y;
   int64_t rows;
   int dev;
+  bool no_slot = false;  // a cache without a slot is not the same as none
 };
 void selective(PyObject* const* a, int64_t nseq, Selective* s) {
   const at::Tensor& x = first(a[0], "x", 2);
@@ -263,6 +267,7 @@ void selective(PyObject* const* a, int64_t nseq, Selective* s) {
     if (t.dim() != 3) refuse(PyExc_ValueError, "state must be a tensor [nslots, dim, dstate]");
     k.nslots = t.size(0);
     k.state = whole<float>(a[9], "state", at::kFloat, {k.nslots, dim, N}, dev);
+    s->no_slot = k.nslots == 0 && (nseq < 0 ? rows : nseq) > 0;
   }
   k.slots = slot_arg(a[10], nseq < 0 ? rows : nseq, dev);
   s->y = output(a[11], x, shape, given(a[11]) ? at::kFloat : dtype_arg(a[12]));
@@ -285,6 +290,7 @@ PyObject* selective_scan_varlen(PyObject* const* a) {
   const Seqs q = seqs(a[13], a[14], x.get_device());
   Selective s;
   selective(a, q.nseq, &s);
+  if (s.no_slot) return PyLong_FromLong(SSD_ERR_INVALID_ARG);
   const int64_t longest = int_arg(a[15], "max_seqlen");
   size_t need = q.nseq > 0 ? p_ssd_selective_varlen_workspace_size(
                                  s.rows, q.nseq, s.args.dim, s.args.dstate, s.args.ngroups, longest)
@@ -308,6 +314,7 @@ PyObject* selective_scan_varlen(PyObject* const* a) {
 PyObject* selective_step(PyObject* const* a) {
   Selective s;
   selective(a, -1, &s);
+  if (s.no_slot) return PyLong_FromLong(SSD_ERR_INVALID_ARG);
   return result(on_device(s.dev, [&](cudaStream_t st) {
                   return p_ssd_selective_step(&s.args, s.rows, st);
                 }),

@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
     if (K > 1 && a.state) {
       for (int i0 = 0; i0 < a.nseq; i0 += 32) {
         const int i = i0 + lane;
-        const bool z = i < a.nseq && a.cu[i] == a.cu[i + 1] && !(a.resume && a.resume[i]);
+        const bool z = i < a.nseq && a.cu[i] == a.cu[i + 1] && !(a.resume && a.resume[i]) &&
+                       !(a.slots && a.slots[i] < 0);
         unsigned m = __ballot_sync(0xffffffffu, z);
         while (m) {
           const int j = i0 + __ffs(m) - 1;
@@ -292,10 +293,9 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
   for (int j = 0; j < VW; ++j) bv[j] = live && a.bias ? a.bias[c0 + j] : 0.f;
 
   for (int64_t r = r0; seq < a.nseq; ++seq) {
-    const int64_t s = a.cu[seq], e0 = a.cu[seq + 1];
+    const int64_t s = a.cu[seq], e = a.cu[seq + 1];
     if (s >= r1) break;
-    const int64_t e = e0 < a.ntok ? e0 : a.ntok;
-    if (e <= s || e <= r0 || s < 0) continue;
+    if (e <= s || e <= r0 || s < 0 || e > a.ntok) continue;
     const bool head = s >= r0;  // the sequence starts in this run
     // rows of this piece: from the sequence's start, or from the run's start but not the rows
     // that belong to the run of the start; and, at a start, at least the first K-1 rows
