@@ -68,10 +68,11 @@ void launch_conv(const ssd::cache::ConvArgs<T>& a, cudaStream_t stream) {
 template <typename T, int K, int VW>
 void launch_conv_step(const ssd::cache::ConvArgs<T>& a, cudaStream_t stream) {
   const unsigned ncb = unsigned((a.cdim + 128 * VW - 1) / (128 * VW));
-  // four rows per thread where that still leaves every SM a few CTAs
-  if (a.ntok / 4 * ncb >= 2 * int64_t(sm_count()))
-    ssd::cache::conv_step_kernel<T, K, VW, 4>
-        <<<dim3(unsigned((a.ntok + 3) / 4), ncb), 128, 0, stream>>>(a);
+  // two rows per thread where that still leaves every SM a few CTAs (256 rows of 5376 channels: 7.0
+  // us with two rows and four channels a thread, 7.3 with two and two, 7.9 with four and two)
+  if (a.ntok / 2 * ncb >= 2 * int64_t(sm_count()))
+    ssd::cache::conv_step_kernel<T, K, VW, 2>
+        <<<dim3(unsigned((a.ntok + 1) / 2), ncb), 128, 0, stream>>>(a);
   else
     ssd::cache::conv_step_kernel<T, K, VW, 1><<<dim3(unsigned(a.ntok), ncb), 128, 0, stream>>>(a);
 }
@@ -83,7 +84,7 @@ void launch_conv_k(const ssd::cache::ConvArgs<T>& a, int kwidth, bool wide, bool
   case KW:                                                                       \
     if (step) {                                                                  \
       if constexpr (KW > 1) {                                                    \
-        if (wide) launch_conv_step<T, KW, 2>(a, stream);                         \
+        if (wide) launch_conv_step<T, KW, 4>(a, stream);                         \
         else launch_conv_step<T, KW, 1>(a, stream);                              \
       }                                                                          \
     } else if (wide) {                                                           \
@@ -332,7 +333,7 @@ NormPlan make_norm_plan(int64_t rows, int cdim, int ngroups, bool wide, int vecs
   if (units <= 128) {
     p.threads = 128;
     p.lanes = units <= 8 ? 8 : 32;
-    p.nv = units <= 32 ? 1 : units <= 64 ? 2 : 4;
+    p.nv = units <= 32 ? 1 : units <= 64 ? 2 : units <= 96 && wide ? 3 : 4;
     if (p.lanes == 8 && !wide) p.lanes = 32;
     if (!wide && p.nv == 2) p.nv = 4;
   } else {
@@ -365,7 +366,8 @@ NormPlan make_norm_plan(int64_t rows, int cdim, int ngroups, bool wide, int vecs
 }
 
 #define SSD_NORM_VARIANTS(X)                                                                  \
-  X(8, 1, 8, 128, 8) X(32, 1, 8, 128, 8) X(32, 2, 8, 128, 4) X(32, 4, 8, 128, 2)              \
+  X(8, 1, 8, 128, 8) X(32, 1, 8, 128, 8) X(32, 2, 8, 128, 4) X(32, 3, 8, 128, 4)              \
+  X(32, 4, 8, 128, 3)                                                                         \
   X(0, 1, 8, 256, 4) X(0, 2, 8, 320, 2) X(0, 2, 8, 512, 1) X(0, 2, 8, 1024, 1)                \
   X(32, 1, 1, 128, 8) X(32, 4, 1, 128, 8) X(0, 4, 1, 512, 2) X(0, 8, 1, 1024, 1)
 

