@@ -124,6 +124,34 @@ struct Raw {
       }
     }
   }
+  // The same through shared memory: pieces of 16 (or one of 8) bytes by asynchronous copies, a
+  // lane's own, 32 lanes to a piece
+  static constexpr int kPieces = VEC ? (kWords + 3) / 4 : 0;
+  __device__ __forceinline__ static void copy(uint32_t to, const T* p) {
+    static_assert(kWords == 2 || kWords % 4 == 0, "whole pieces");
+    const unsigned char* q = reinterpret_cast<const unsigned char*>(p);
+    if constexpr (kWords == 2) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(q) : "memory");
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * k),
+                     "l"(q + 16 * k)
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ void take(const uint4* from) {
+    if constexpr (kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(from);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const uint4 v = from[32 * k];
+        w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+      }
+    }
+  }
   __device__ __forceinline__ void load1(int i, const T* p) {  // one value per word
     if constexpr (sizeof(T) == 2) w[i] = *reinterpret_cast<const unsigned short*>(p);
     else w[i] = *reinterpret_cast<const uint32_t*>(p);

@@ -87,8 +87,8 @@ __device__ __forceinline__ float softplus_acc(float v) {
 // and SM, or 256 where a warp reads one or two addresses, and every lane reads its states' B and
 // C anew; with four lanes of four states that takes longer than the exponentials.
 // Measured, 5120 bf16 channels, 16 states, softplus and gate: four prompts of about 4000 tokens in
-// 567 us, 66% of the ex2 rate; ragged ones are bound by the longest, at 92 ns a token.  One prompt of
-// 16384 tokens and 1536 channels, in chunks: 296 us.
+// 537 us, 69% of the ex2 rate; ragged ones are bound by the longest, at 79 ns a token.  One prompt of
+// 16384 tokens and 1536 channels, in chunks: 285 us.
 constexpr int kStage = 16;
 
 // The sequence that `rank` others come before, by falling length; nseq <= kSorted.  Call with the
@@ -137,6 +137,16 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
   __shared__ __align__(16) float2 du[2][kStage * CH];
   __shared__ __align__(16) float bsm[2][kStage * NP], csm[2][SUMMARY ? 4 : kStage * NP];
   __shared__ __align__(16) float ysm[2][SUMMARY ? 4 : kStage * 32];
+  using RawX = Raw<T, EX, VEC>;
+  using RawD = Raw<TD, EX, VEC>;
+  using RawB = Raw<T, EB, VEC>;
+  // Wide loads of bf16 rows go through a ring in shared memory, kRing stages deep (ragged prompts at
+  // 5120 channels: 843 -> 724 us, even ones 567 -> 537).  Float32 rows fill twice the ring and the
+  // copies' time: 317 -> 351 us even, 36 -> 42 us for 33 short ones; they go into registers.
+  constexpr bool RING = VEC && sizeof(T) == 2;
+  constexpr int kRing = 2;
+  constexpr int kSlot = RING ? 32 * (2 * RawX::kPieces + RawD::kPieces + 2 * RawB::kPieces) : 1;
+  __shared__ __align__(16) uint4 ring[RING ? kRing * kSlot : 1];
   // place of channel c in the rows of token k: what lanes on the same channels of eight rows touch
   // together lies on banks of its own
   auto place = [](int k, int c) { return c ^ (k & (CH < 8 ? CH - 1 : 7)); };
@@ -322,22 +332,41 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
   auto left_of = [&](int64_t st) {
     return rows - st * kStage > kStage ? kStage : int(rows - st * kStage);
   };
-  Raw<T, EX, VEC> rx, rz;
-  Raw<TD, EX, VEC> rd;
-  Raw<T, EB, VEC> rb, rc;
+  RawX rx, rz;
+  RawD rd;
+  RawB rb, rc;
   // D x and the gate of the two stages that are not finished
   float skip0[EX], skip1[EX], gate0[EX], gate1[EX];
-  auto load = [&](int64_t st) {  // rows past the end read the last one again
-    if (st >= nst) return;
-    const int left = left_of(st);
-    if constexpr (VEC) {
-      const int64_t r = min(row0, left - 1);
+  // Loads of stage st, into the ring, where the lane finds them when the stage is prepared, or into
+  // registers, one stage ahead.  Rows past the end read the last one again.
+  auto load = [&](int64_t st) {
+    if constexpr (RING) {
+      if (st < nst) {
+        const int64_t r = min(row0, left_of(st) - 1);
+        uint32_t to = uint32_t(__cvta_generic_to_shared(ring + (st % kRing) * kSlot + lane));
+        RawX::copy(to, px + r * a.xs);
+        to += 512 * RawX::kPieces;
+        RawD::copy(to, pt + r * a.dts);
+        to += 512 * RawD::kPieces;
+        RawB::copy(to, pb + r * a.bs + bn);
+        to += 512 * RawB::kPieces;
+        if (!SUMMARY) RawB::copy(to, pc + r * a.cs + bn);
+        to += 512 * RawB::kPieces;
+        if (gate) RawX::copy(to, pz + r * a.zs);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (st >= nst) return;
+    } else if constexpr (VEC) {
+      if (st >= nst) return;
+      const int64_t r = min(row0, left_of(st) - 1);
       rx.load(px + r * a.xs);
       rd.load(pt + r * a.dts);
       if (gate) rz.load(pz + r * a.zs);
       rb.load(pb + r * a.bs + bn);
       if (!SUMMARY) rc.load(pc + r * a.cs + bn);
     } else {
+      if (st >= nst) return;
+      const int left = left_of(st);
 #pragma unroll
       for (int i = 0; i < EX; ++i) {
         const int64_t r = min(row0 + i * RX, left - 1);
@@ -362,6 +391,19 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
   float Dd[VEC ? EX : 1], bias[VEC ? EX : 1];
   auto prepare = [&](int64_t st) {
     const int left = left_of(st), buf = int(st & 1);
+    if constexpr (RING) {  // the kRing - 1 stages after this one may still be on their way
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      const uint4* from = ring + (st % kRing) * kSlot + lane;
+      rx.take(from);
+      from += 32 * RawX::kPieces;
+      rd.take(from);
+      from += 32 * RawD::kPieces;
+      rb.take(from);
+      from += 32 * RawB::kPieces;
+      if (!SUMMARY) rc.take(from);
+      from += 32 * RawB::kPieces;
+      if (gate) rz.take(from);
+    }
     constexpr int E2 = EX > 1 ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < EX; i += E2) {
@@ -467,21 +509,27 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
   };
 
   load(0);
+  if constexpr (RING) {
+#pragma unroll
+    for (int st = 1; st < kRing; ++st) load(st);
+  }
 #pragma unroll
   for (int i = 0; i < (VEC ? EX : 1); ++i) {
     Dd[i] = !SUMMARY && eon && a.D ? a.D[ec + i] : 0.f;
     bias[i] = eon && a.dt_bias ? a.dt_bias[ec + i] : 0.f;
   }
+  constexpr int kNext = RING ? kRing : 1;  // stages between a load and its preparation
   if (nst > 0) prepare(0);
-  load(1);
+  load(kNext);
   __syncthreads();
   for (int64_t st = 0; st < nst; ++st) {  // the other warp is on stage st
     if (!SUMMARY && st > 0) finish(st - 1, skip0, gate0);
     if (st + 1 < nst) prepare(st + 1);
-    load(st + 2);
+    load(st + 1 + kNext);
     __syncthreads();
   }
   if (!SUMMARY && nst > 0) finish(nst - 1, skip1, gate1);
+  if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // One token of each sequence.  LPC lanes per channel with 4 states each, a warp on 32 / LPC
