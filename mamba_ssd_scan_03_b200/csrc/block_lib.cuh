@@ -581,7 +581,8 @@ ssd_status ssd_group_norm_gate_bwd(const void* dout, int64_t dout_stride, const 
     if (st != SSD_OK) return st;
   }
   const int per = bias ? 2 : 1;
-  ssd::norm::norm_sum_kernel<<<dim3(unsigned((cdim + 31) / 32), unsigned(per)), 256, 0, stream>>>(
+  ssd::norm::norm_sum_kernel<<<dim3(unsigned((cdim + 31) / 32), unsigned(per)),
+                              32 * ssd::norm::kSumRows, 0, stream>>>(
       static_cast<const float*>(workspace), int(p.cta_rows), per, cdim, dweight, dbias);
   return launched();
 }

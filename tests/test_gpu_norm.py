@@ -205,3 +205,20 @@ def test_norm_refuses():
         ssd.group_norm_gate(y.t(), torch.ones(4, device="cuda"))
     with pytest.raises(TypeError):
         ssd.group_norm_gate(y.half(), w)
+
+
+@pytest.mark.parametrize("rows,C", [(700, 16384), (700, 8192), (1300, 4096), (2500, 640)])
+def test_norm_rows_in_many_rounds(rows, C):
+    """Rows that take the CTAs several rounds, through rings of one, two and three rows: the same
+    values, bit for bit, as in calls of few rows, which need no ring."""
+    g = inputs(rows, C, "f32", "f32", seed=8)
+    do = torch.from_numpy(np.random.default_rng(9).standard_normal((rows, C)).astype(np.float32))
+    y, z, w, b, do = up(g["y"]), up(g["z"]), up(g["w"]), up(g["b"]), do.cuda()
+    out = ssd.group_norm_gate(y, w, b, z, 1)
+    grads = ssd.group_norm_gate_bwd(do, y, w, b, z, 1)
+    for lo in range(0, rows, 100):
+        s = slice(lo, min(lo + 100, rows))
+        assert torch.equal(out[s], ssd.group_norm_gate(y[s], w, b, z[s], 1))
+        part = ssd.group_norm_gate_bwd(do[s], y[s], w, b, z[s], 1)
+        assert torch.equal(grads["y"][s], part["y"]) and torch.equal(grads["z"][s], part["z"])
+    assert ssd.device_status() == 0
