@@ -1,7 +1,7 @@
 // binding.cpp -- the Python binding of the served forms and the norm (include/ssd.h) as a CPython
 // extension: checks tensors, allocates outputs and workspace with PyTorch, and passes raw
 // pointers plus the current CUDA stream.  A token's call is mostly host time: the same checks
-// through ctypes took 13 to 17 us a call, here 6 to 8.  No kernel and no computation is here; the C
+// through ctypes took 13 to 17 us a call, here 6 to 7.  No kernel and no computation is here; the C
 // entries are looked up in the library that the package has loaded.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAGuard.h>

@@ -176,8 +176,8 @@ SelPlan make_sel_plan(int64_t ntok, int nseq, int dim, int dstate, int ngroups, 
   p.units = nseq;
   if (warps < sched && len >= 128) {
     // two full rounds of CTAs (eight to an SM), chunks of at least 64 tokens.  One prompt of 16384
-    // tokens and 1536 channels: 301 us, 366 with half as many chunks, 342 with three times as many,
-    // 1020 uncut; of 8192 and 5120: 486, 614, 484
+    // tokens and 1536 channels: 301 us, 366 with a quarter as many chunks, 342 with three times as
+    // many, 1020 uncut; of 8192 and 5120: 486, 614, 484 (before rows came through the ring)
     const int64_t want = std::min(4 * sched / warps, len / 64);
     if (want > 2) {
       p.chunk = int((len + want - 1) / want + 15) / 16 * 16;
