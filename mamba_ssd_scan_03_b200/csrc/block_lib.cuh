@@ -414,6 +414,11 @@ ssd_status launch_norm(const NormPlan& p, const ssd::norm::NormArgs& a, bool bwd
   return SSD_ERR_UNSUPPORTED;
 }
 
+// Eight channels at a time: whole units in a group, and the weight, which is read in 16-byte accesses
+// too (the bias is read value by value).  The rows have their own conditions.
+bool norm_wide(int cdim, int ngroups, const float* weight) {
+  return (cdim / ngroups) % 8 == 0 && aligned16(weight);
+}
 bool norm_shape_ok(int64_t rows, int cdim, int ngroups) {
   return rows >= 0 && cdim >= 1 && ngroups >= 1 && cdim % ngroups == 0;
 }
@@ -511,7 +516,8 @@ ssd_status ssd_group_norm_gate(const void* y, int64_t y_stride, const float* wei
                     in_place ? Arg{nullptr, 0} : rows_arg(y, rows, y_stride, cdim, ey)};
   const Arg outs[] = {rows_arg(out, rows, out_stride, cdim, eo)};
   if (!args_ok(in, outs)) return SSD_ERR_INVALID_ARG;
-  const bool wide = (cdim / ngroups) % 8 == 0 && rows16(y, y_stride, ey) && y_stride % 8 == 0 &&
+  const bool wide = norm_wide(cdim, ngroups, weight) && rows16(y, y_stride, ey) &&
+                    y_stride % 8 == 0 &&
                     (!z || (rows16(z, z_stride, ez) && z_stride % 8 == 0)) &&
                     rows16(out, out_stride, eo) && out_stride % 8 == 0;
   ssd::norm::NormArgs a{};
@@ -561,7 +567,8 @@ ssd_status ssd_group_norm_gate_bwd(const void* dout, int64_t dout_stride, const 
                       need ? Arg{workspace, need} : Arg{nullptr, 0}};
   if (rows > 0 && !dy) return SSD_ERR_INVALID_ARG;
   if (!args_ok(in, outs)) return SSD_ERR_INVALID_ARG;
-  const bool wide = (cdim / ngroups) % 8 == 0 && rows16(y, y_stride, ey) && y_stride % 8 == 0 &&
+  const bool wide = norm_wide(cdim, ngroups, weight) && rows16(y, y_stride, ey) &&
+                    y_stride % 8 == 0 &&
                     (!z || (rows16(z, z_stride, ez) && z_stride % 8 == 0 && aligned16(dz))) &&
                     rows16(dout, dout_stride, eo) && dout_stride % 8 == 0 && aligned16(dy);
   ssd::norm::NormArgs a{};
