@@ -290,36 +290,43 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
     }
   }
 
-  // the first sequence that ends after r0
+  // the first sequence that ends after r0; with bounds that fall or leave the rows, where counting
+  // says nothing, all sequences are looked at
   int seq = 0;
-  {
-    int n = 0;
-    for (int i0 = 0; i0 < a.nseq; i0 += 32) {
-      const int i = i0 + lane;
-      n += __popc(__ballot_sync(0xffffffffu, i < a.nseq && a.cu[i + 1] <= r0));
+  bool ordered = true;
+  for (int i0 = 0; i0 < a.nseq; i0 += 32) {
+    const int i = i0 + lane;
+    bool before = false;
+    if (i < a.nseq) {
+      const int s = a.cu[i], e = a.cu[i + 1];
+      before = e <= r0;
+      ordered &= s >= 0 && s <= e && e <= a.ntok;
     }
-    seq = n;
+    seq += __popc(__ballot_sync(0xffffffffu, before));
   }
+  ordered = __all_sync(0xffffffffu, ordered);
+  if (!ordered) seq = 0;
 
   float wr[VW][K], bv[VW];
   load_w<K, VW>(a.w + int64_t(live ? c0 : 0) * K, wr);
 #pragma unroll
   for (int j = 0; j < VW; ++j) bv[j] = live && a.bias ? a.bias[c0 + j] : 0.f;
 
-  for (int64_t r = r0; seq < a.nseq; ++seq) {
+  for (; seq < a.nseq; ++seq) {
     const int64_t s = a.cu[seq], e = a.cu[seq + 1];
-    if (s >= r1) break;
+    if (s >= r1) {
+      if (ordered) break;
+      continue;
+    }
     if (e <= s || e <= r0 || s < 0 || e > a.ntok) continue;
     const bool head = s >= r0;  // the sequence starts in this run
     // rows of this piece: from the sequence's start, or from the run's start but not the rows
     // that belong to the run of the start; and, at a start, at least the first K-1 rows
-    int64_t b = head ? s : (s + K - 1 > r0 ? s + K - 1 : r0);
+    const int64_t b = head ? s : (s + K - 1 > r0 ? s + K - 1 : r0);
     int64_t end = e < r1 ? e : r1;
     if (head && s + K - 1 > end) end = s + K - 1 < e ? s + K - 1 : e;
-    if (b < r) b = r;  // rows of one piece never come before another's
     const int64_t slot = a.state || a.slots ? warp_slot(a.slots, seq, a.nslots) : 0;
     if (slot < 0 || b >= end) continue;
-    r = end;
 
     float win[W][VW];
 #pragma unroll

@@ -1,0 +1,70 @@
+"""Packed prompts whose bounds fall or leave the rows: such sequences are left out and reported, the
+rows and slots of all others are as in calls of their own (rows that two sequences name may hold
+either's)."""
+import numpy as np
+import pytest
+import torch
+
+import mamba_ssd_scan_03_b200 as ssd
+from oracle import served
+from served_util import conv_bound, down, excess, up
+from test_gpu_served import conv_inputs, flags, i32
+
+pytestmark = pytest.mark.gpu
+
+INDEX = 6
+
+
+def whole_sequences(cu, ntok):
+    """The sequences to scan, and how many of them name each row."""
+    ok = [i for i in range(len(cu) - 1) if 0 <= cu[i] <= cu[i + 1] <= ntok]
+    named = np.zeros(ntok, int)
+    for i in ok:
+        named[cu[i]:cu[i + 1]] += 1
+    return ok, named
+
+
+def check_conv(cu, T, C, K, io="f32", seed=0):
+    n = len(cu) - 1
+    r = np.random.default_rng(seed)
+    g = conv_inputs(T, C, K, n + 2, io, seed)
+    slots = [int(s) for s in r.permutation(n + 2)[:n]]
+    resume = [bool(v) for v in r.integers(0, 2, n)]
+    st = up(g["state"], io)
+    out = torch.full((T, C), 5.0, device="cuda", dtype=st.dtype)
+    ssd.conv_silu_varlen(up(g["u"], io), up(g["w"]), i32(cu), up(g["bias"]), st, i32(slots),
+                         flags(resume), out=out)
+    status = ssd.device_status()
+    ok, named = whole_sequences(cu, T)
+    got, rst = down(out), down(up(g["state"], io))
+    assert np.all(got[named == 0] == 5.0)
+    for i in ok:
+        one = ([cu[i], cu[i + 1]], g["state"], [slots[i]], [resume[i]])
+        ref, state = served.conv_silu(g["u"], g["w"], g["bias"], *one)
+        bound = conv_bound(g["u"], g["w"], g["bias"], *one, io)
+        rows = [t for t in range(cu[i], cu[i + 1]) if named[t] == 1]
+        worst = excess(got[rows], ref[rows], bound[rows])
+        assert worst <= 0, (cu, i)
+        rst[slots[i]] = state[slots[i]]
+    assert [s for s in range(n + 2) if not np.array_equal(down(st)[s], rst[s])] == []
+    assert status == (0 if len(ok) == n else INDEX)
+
+
+BIG = 2 ** 31 - 1
+BOUNDS = [
+    (100, [0, 200, 20, 30, 100]),             # past the rows, then back
+    (300, [0, 100, 400, 200, 300]),
+    (300, [0, 100, -5, 200, 300]),            # before the rows
+    (300, [0, 250, 40, 290]),                 # rows named twice
+    (300, [0, 120, 120, 300, 0, 0, 10]),      # and a start over
+    (300, [0, BIG, -BIG - 1, 10, 300]),
+    (300, [300, 0, 300]),
+    (64, [70, 60, 50, 40, 30, 20, 10, 0]),    # nothing but falls
+]
+
+
+@pytest.mark.parametrize("T,cu", BOUNDS)
+@pytest.mark.parametrize("C,K", [(40, 4), (33, 2), (8, 8)])
+def test_conv_leaves_out_only_bad_sequences(T, cu, C, K):
+    check_conv(cu, T, C, K, seed=len(cu))
+    check_conv(cu, T, C, K, "bf16", seed=len(cu) + 1)
