@@ -270,12 +270,12 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
 
   if (run == 0) {
     if (cb == 0) warp_check_seqs(a.cu, a.nseq, a.ntok);
-    // sequences of length zero have no first row: a fresh one leaves a history of zeros
+    // sequences of length zero have no first row: a fresh one (on the rows) leaves a history of zeros
     if (K > 1 && a.state) {
       for (int i0 = 0; i0 < a.nseq; i0 += 32) {
         const int i = i0 + lane;
-        const bool z = i < a.nseq && a.cu[i] == a.cu[i + 1] && !(a.resume && a.resume[i]) &&
-                       !(a.slots && a.slots[i] < 0);
+        const bool z = i < a.nseq && a.cu[i] == a.cu[i + 1] && a.cu[i] >= 0 && a.cu[i] <= a.ntok &&
+                       !(a.resume && a.resume[i]) && !(a.slots && a.slots[i] < 0);
         unsigned m = __ballot_sync(0xffffffffu, z);
         while (m) {
           const int j = i0 + __ffs(m) - 1;

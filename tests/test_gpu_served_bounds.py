@@ -68,3 +68,12 @@ BOUNDS = [
 def test_conv_leaves_out_only_bad_sequences(T, cu, C, K):
     check_conv(cu, T, C, K, seed=len(cu))
     check_conv(cu, T, C, K, "bf16", seed=len(cu) + 1)
+
+
+@pytest.mark.parametrize("T,cu", [(12, [0, 9, 13, 13]), (12, [-3, -3, 0, 12]), (12, [5, 5, 12, 12]),
+                                  (12, [0, 12, 12, 13, 13, 12, 12])])
+@pytest.mark.parametrize("C,K", [(40, 4), (33, 2)])
+def test_conv_of_empty_sequences_off_the_rows(T, cu, C, K):
+    """An empty fresh sequence clears its slot; not so where its bounds lie off the rows."""
+    for seed in range(4):
+        check_conv(cu, T, C, K, seed=seed)
