@@ -477,7 +477,6 @@ ssd_status ssd_selective_scan_varlen(const ssd_selective_args* args, const int32
   k.ntok = ntok;
   k.nseq = nseq;
   k.chunk = p.chunk;
-  k.nunits = int(std::min<int64_t>(p.units, INT32_MAX));
   if (need) {
     k.ws_state = static_cast<float*>(workspace);
     k.ws_dt = reinterpret_cast<float*>(

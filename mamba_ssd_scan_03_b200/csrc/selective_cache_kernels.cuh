@@ -40,7 +40,6 @@ struct SelArgs {
   int64_t ntok, nslots;
   int nseq, dim, dstate, ngroups;
   int chunk;   // tokens per unit (0: a unit is a whole sequence)
-  int nunits;  // units the workspace has room for: ntok / chunk + nseq
   bool io_bf16, dt_bf16, y_bf16, softplus;
   bool by_length;  // whole sequences only, at most kSorted: the longest come first
 };
@@ -180,12 +179,14 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
   if (a.chunk) {
     seq = -1;
     int base = 0;
-    for (int i0 = 0; i0 < a.nseq && seq < 0; i0 += 32) {
+    bool ordered = true;
+    for (int i0 = 0; i0 < a.nseq; i0 += 32) {
       const int i = i0 + lane;
       int n = 0;
       if (i < a.nseq) {
-        const int64_t len = int64_t(a.cu[i + 1]) - a.cu[i];
-        n = len <= 0 ? 1 : int((min(len, a.ntok) + a.chunk - 1) / a.chunk);
+        const int s = a.cu[i], e = a.cu[i + 1];
+        ordered &= s >= 0 && s <= e && e <= a.ntok;
+        n = e > s ? int((min(int64_t(e) - s, a.ntok) + a.chunk - 1) / a.chunk) : 1;
       }
       int incl = n;
 #pragma unroll
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
         if (lane >= o) incl += v;
       }
       const unsigned m = __ballot_sync(0xffffffffu, unit < base + incl && i < a.nseq);
-      if (m) {
+      if (m && seq < 0) {
         const int l = __ffs(m) - 1;
         seq = i0 + l;
         nchunk = __shfl_sync(0xffffffffu, n, l);
@@ -202,8 +203,14 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
       }
       base = min(base + __shfl_sync(0xffffffffu, incl, 31), 1 << 30);
     }
-    // bounds that do not increase can name more chunks than there is room for (latched above)
-    if (seq < 0 || unit - chunk + nchunk > a.nunits) return;
+    // bounds that fall or leave the rows can name more chunks than there is room for: with them
+    // every sequence is one unit
+    if (!__all_sync(0xffffffffu, ordered)) {
+      seq = unit < a.nseq ? unit : -1;
+      chunk = 0;
+      nchunk = 1;
+    }
+    if (seq < 0) return;
   }
   if (SUMMARY && nchunk == 1) return;
   const int64_t s0 = a.cu[seq], s1 = a.cu[seq + 1];
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
 
   if (SUMMARY && last) return;  // no chunk after it asks
   const int64_t t0 = s0 + int64_t(chunk) * a.chunk;
-  const int64_t t1 = a.chunk && t0 + a.chunk < s1 ? t0 + a.chunk : s1;
+  const int64_t t1 = last ? s1 : t0 + a.chunk;
   const int64_t rows = t1 - t0;
   const int64_t nst = (rows + kStage - 1) / kStage;
 
