@@ -503,8 +503,9 @@ __global__ void __launch_bounds__(MAXT, MINB) group_norm_bwd_kernel(const NormAr
           if (a.z) {
             const float2 zz = pair<VW>(z, j), sg = sigmoid2(zz);
             g = mul2(zz, sg);
-            // silu' = sg (1 + z (1 - sg)) = sg + g - g sg
-            slope = fma2(make_float2(-g.x, -g.y), sg, cache::add2(sg, g));
+            // silu' = sg (1 + z (1 - sg)) = sg + g (1 - sg).  Not as (sg + g) - g sg: both are of the
+            // gate's size, and past 2^24 the 1 between them is lost.
+            slope = fma2(g, cache::add2(dup(1.f), make_float2(-sg.x, -sg.y)), sg);
             if (first) v = mul2(yy, g);
           }
           const float2 n = mul2(cache::add2(v, dup(-mu)), r2);
