@@ -446,7 +446,8 @@ typedef struct {
  *   plan, never the result's rows.  Where there are few channels and sequences for the GPU, sequences
  *   are cut into chunks: one launch finds the state after each chunk, a second scans the chunks
  *   from their entering states.  workspace: ssd_selective_varlen_workspace_size() bytes for the
- *   same shape (0 is possible), 256-byte aligned, contents on entry ignored. */
+ *   same shape (0 is possible), asked for with the same device current (the plan follows its SMs),
+ *   256-byte aligned, contents on entry ignored. */
 size_t ssd_selective_varlen_workspace_size(int64_t ntok, int nseq, int dim, int dstate,
                                            int ngroups, int64_t max_seqlen);
 ssd_status ssd_selective_scan_varlen(const ssd_selective_args* args, const int32_t* cu_seqlens,
@@ -480,7 +481,8 @@ ssd_status ssd_group_norm_gate(const void* y, int64_t y_stride, const float* wei
  *   forward (bias NULL: no dbias); dout [rows, cdim] in dout_dtype.  Outputs: dy [rows, cdim]
  *   float32 and dz [rows, cdim] in z_dtype (NULL where z is), dense; dweight, dbias [cdim] float32.
  *   The statistics are found again from y and z.  Sums over rows in a fixed order.  workspace:
- *   ssd_group_norm_gate_bwd_workspace_size() bytes, 256-byte aligned. */
+ *   ssd_group_norm_gate_bwd_workspace_size() bytes, asked for with the same device current,
+ *   256-byte aligned. */
 size_t ssd_group_norm_gate_bwd_workspace_size(int64_t rows, int cdim, int ngroups);
 ssd_status ssd_group_norm_gate_bwd(const void* dout, int64_t dout_stride, const void* y,
                                    int64_t y_stride, const float* weight, const float* bias,

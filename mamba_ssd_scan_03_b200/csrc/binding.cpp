@@ -160,10 +160,16 @@ const int32_t* slot_arg(PyObject* o, int64_t n, int dev) {
   return whole<int32_t>(o, "slots", at::kInt, {n}, dev);
 }
 
+// Makes the tensors' device current for a scope.  A workspace's size follows the current device's SMs,
+// so its query stands in such a scope, as the launch does.
+struct OnDevice {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit OnDevice(int dev) : guard(c10::Device(c10::kCUDA, dev)) {}
+};
 // Calls a C entry with the device current, on its current stream.
 template <typename F>
 int on_device(int dev, const F& call) {
-  const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, dev));
+  const OnDevice here(dev);
   return int(call(c10::cuda::getCurrentCUDAStream(dev).stream()));
 }
 // The output, or the status of a call that was refused.
@@ -292,6 +298,7 @@ PyObject* selective_scan_varlen(PyObject* const* a) {
   selective(a, q.nseq, &s);
   if (s.no_slot) return PyLong_FromLong(SSD_ERR_INVALID_ARG);
   const int64_t longest = int_arg(a[15], "max_seqlen");
+  const OnDevice here(s.dev);
   size_t need = q.nseq > 0 ? p_ssd_selective_varlen_workspace_size(
                                  s.rows, q.nseq, s.args.dim, s.args.dstate, s.args.ngroups, longest)
                            : 0;
@@ -387,6 +394,7 @@ PyObject* group_norm_gate_bwd(PyObject* const* a) {
   at::Tensor dy = at::empty(shape, f32), dw = at::empty({n.cdim}, f32), dz, db, ws;
   if (given(a[3])) dz = at::empty(shape, f32.dtype(n.zd == SSD_BF16 ? at::kBFloat16 : at::kFloat));
   if (n.b) db = at::empty({n.cdim}, f32);
+  const OnDevice here(n.dev);
   void* wp = nullptr;
   size_t need = p_ssd_group_norm_gate_bwd_workspace_size(n.rows, n.cdim, n.ngroups);
   if (given(a[9])) {
