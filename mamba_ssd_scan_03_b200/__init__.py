@@ -10,12 +10,17 @@ path: if the library is missing or no CUDA device is present, the calls raise.
 """
 import ctypes
 import os
+import sys
+from importlib import machinery, util
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssd.so")
-BINDING_PATH = os.path.join(_HERE, "_binding.so")
+# The compiled binding holds to the ABI of one Python and one torch: its name says which, and under
+# others it counts as missing.
+BINDING_PATH = os.path.join(
+    _HERE, f"_binding.{sys.implementation.cache_tag}.torch-{torch.__version__}.so")
 
 SSD_F32, SSD_BF16 = 0, 1
 SSD_PATH_SIMT, SSD_PATH_TCGEN05 = 0, 1
@@ -547,9 +552,11 @@ def _call(name, *args):
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
                                "`python -m mamba_ssd_scan_03_b200.build`")
-        from . import _binding
-        _binding.bind(LIB_PATH)
-        _served = _binding
+        loader = machinery.ExtensionFileLoader(__name__ + "._binding", BINDING_PATH)
+        binding = util.module_from_spec(util.spec_from_loader(loader.name, loader))
+        loader.exec_module(binding)
+        binding.bind(LIB_PATH)
+        _served = binding
     out = getattr(_served, name)(*args)
     if out.__class__ is int:
         raise SSDError(out, "ssd_" + name)

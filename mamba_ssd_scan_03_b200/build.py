@@ -1,5 +1,5 @@
-"""Build libssd.so (the sm_100a CUDA library behind include/ssd.h) and _binding.so (the Python
-binding of its served forms) in-tree.
+"""Build libssd.so (the sm_100a CUDA library behind include/ssd.h) and the Python binding of its
+served forms (_binding.<Python>.<torch>.so) in-tree.
 
 ``python -m mamba_ssd_scan_03_b200.build`` or ``build()``.  One nvcc invocation on the single
 translation unit ``csrc/ssd_lib.cu`` and one of the host compiler on ``csrc/binding.cpp``; both land
@@ -9,12 +9,13 @@ import os
 import subprocess
 import sys
 
+from . import BINDING_PATH as BINDING
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssd.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
-BINDING = os.path.join(HERE, "_binding.so")
 CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
