@@ -166,11 +166,21 @@ struct OnDevice {
   c10::cuda::OptionalCUDAGuard guard;
   explicit OnDevice(int dev) : guard(c10::Device(c10::kCUDA, dev)) {}
 };
-// Calls a C entry with the device current, on its current stream.
+// Lets other Python threads run for a scope.
+struct NoGil {
+  PyThreadState* const held = PyEval_SaveThread();
+  NoGil() = default;
+  NoGil(const NoGil&) = delete;
+  ~NoGil() { PyEval_RestoreThread(held); }
+};
+// Calls a C entry with the device current, on its current stream.  Other Python threads run meanwhile: a
+// launch waits where the driver's queue is full, perhaps for work that one of them has to start.
 template <typename F>
 int on_device(int dev, const F& call) {
   const OnDevice here(dev);
-  return int(call(c10::cuda::getCurrentCUDAStream(dev).stream()));
+  const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
+  const NoGil others;
+  return int(call(stream));
 }
 // The output, or the status of a call that was refused.
 PyObject* result(int status, const at::Tensor& out) {

@@ -1,8 +1,10 @@
-"""The compiled binding around the C entries: which device it has made current while it calls them.
-The entries are stand-ins that launch nothing."""
+"""The compiled binding around the C entries: what it holds and which device it has made current
+while it calls them.  The entries are stand-ins that launch nothing."""
 import ctypes
 import os
 import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -15,7 +17,9 @@ pytestmark = pytest.mark.gpu
 STAND_INS = r"""
 #include <dlfcn.h>
 #include <stddef.h>
-static int device = -1;
+#include <unistd.h>
+static volatile int go, device = -1;
+void set_go(int v) { go = v; }
 int queried_on(void) { int d = device; device = -1; return d; }
 static void note(void) {
   void* cuda = dlopen("libcuda.so.1", RTLD_NOW | RTLD_NOLOAD);
@@ -23,7 +27,10 @@ static void note(void) {
   int d = -1;
   if (get && get(&d) == 0) device = d;
 }
-int ssd_conv_silu_step(void) { return 0; }
+int ssd_conv_silu_step(void) {  /* SSD_OK when another thread says go within five seconds */
+  for (int k = 0; k < 5000 && !go; ++k) usleep(1000);
+  return go ? 0 : 4;
+}
 size_t ssd_selective_varlen_workspace_size(void) { note(); return 256; }
 size_t ssd_group_norm_gate_bwd_workspace_size(void) { note(); return 256; }
 int ssd_conv_silu_varlen(void) { return 0; }
@@ -47,6 +54,23 @@ def stand_ins(tmp_path):
     yield fake
     ssd._served.bind(ssd.LIB_PATH)
     assert torch.all(ssd.group_norm_gate(torch.ones(1, 8, device="cuda"), w) > 0.99)
+
+
+def test_other_threads_run_during_a_call(stand_ins):
+    """A launch can wait for room in the driver's queue; other Python threads go on meanwhile, those
+    among them that the GPU's work may be waiting for."""
+    def later():
+        time.sleep(0.1)
+        stand_ins.set_go(1)
+
+    cs, u = torch.zeros(2, 3, 8, device="cuda"), torch.zeros(2, 8, device="cuda")
+    w = torch.zeros(8, 4, device="cuda")
+    other = threading.Thread(target=later)
+    other.start()
+    try:
+        assert ssd.conv_silu_step(cs, u, w).shape == (2, 8)
+    finally:
+        other.join()
 
 
 def test_workspace_is_sized_on_the_tensors_device(stand_ins):
