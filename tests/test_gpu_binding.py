@@ -87,3 +87,44 @@ def test_workspace_is_sized_on_the_tensors_device(stand_ins):
         ssd.group_norm_gate_bwd(y, y, w)
         assert stand_ins.queried_on() == last
         assert torch.cuda.current_device() == 0
+
+
+def test_threads_call_at_once():
+    """Four threads, each on a stream of its own, at the same time:
+    convolution, scan in chunks, norm and gradients give what one thread gets."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    u, w, raw, B = rand(700, 64), rand(64, 4), rand(700, 64), rand(700, 1, 16)
+    A, z, nw, cu = -torch.exp(rand(64, 16)), rand(700, 64), rand(64), i32([0, 690, 700])
+    state = rand(2, 64, 16)
+    torch.cuda.synchronize()
+
+    def block():
+        st = state.clone()
+        x = ssd.conv_silu_varlen(u, w, cu)
+        y = ssd.selective_scan_varlen(x, raw, A, B, B, cu, z=z, softplus=True, state=st)
+        y1 = ssd.selective_step(st, x[:2], raw[:2], A, B[:2], B[:2], softplus=True)
+        n = ssd.group_norm_gate(y, nw, None, z, 4)
+        g = ssd.group_norm_gate_bwd(n, y, nw, None, z, 4)
+        return [x, y, st, y1, n, g["y"], g["z"], g["weight"]]
+
+    got = [[] for _ in range(4)]
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got[k].append(block())
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    want = block()
+    assert [len(r) for r in got] == [20] * 4
+    for r in got:
+        for one in r:
+            assert all(torch.equal(a, b) for a, b in zip(one, want))
+    assert ssd.device_status() == 0
