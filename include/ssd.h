@@ -378,10 +378,10 @@ ssd_status ssd_selective_scan_fwd(const void* x, const float* dt, const float* A
  * written and no slot changes.  A slot past the cache, or one that an earlier sequence of the
  * same call names too, is left out in the same way and latched as SSD_ERR_INDEX, as are bounds
  * that decrease or leave [0, ntok] (ssd_get_device_status reports it; the rows and slots of the
- * other sequences are then as usual, but for rows that such bounds name twice).  resume[i] (one byte, device memory; NULL: all zero) says
- * whether prompt i continues from its slot (nonzero) or starts from zeros; either way the slot
- * holds the state after the prompt when the call is done.  An empty prompt that resumes leaves
- * its slot as it was.
+ * other sequences are then as usual, but for rows that such bounds name twice).  resume[i] (one
+ * byte, device memory; NULL: all zero) says whether prompt i continues from its slot (nonzero) or
+ * starts from zeros; either way the slot holds the state after the prompt when the call is done.
+ * An empty prompt that resumes leaves its slot as it was.
  *
  * All of it is read by the kernels, so the calls can be captured and replayed with new bounds,
  * slots and flags.  Outputs must not overlap inputs (taken over their whole extent, first row

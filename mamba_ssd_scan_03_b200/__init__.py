@@ -571,9 +571,9 @@ def conv_silu_varlen(u, w, cu_seqlens, bias=None, conv_state=None, slots=None, r
 
     conv_state [nslots,K-1,C] in u's dtype holds each slot's last K-1 inputs and is updated in
     place; slots [nseq] int32 (None: sequence i has slot i; negative: padding, left alone); resume
-    [nseq] bool says which sequences continue from their slot (None: none).  Rows outside the
-    sequences are not written.  Bad slots and bounds are left out and reported by
-    device_status()."""
+    [nseq] bool says which sequences continue from their slot (None: none).  A width K of 1 has no
+    history: no conv_state, slots or resume.  Rows outside the sequences are not written.  Bad slots
+    and bounds are left out and reported by device_status()."""
     return _call("conv_silu_varlen", u, w, cu_seqlens, bias, conv_state, slots, resume, out)
 
 

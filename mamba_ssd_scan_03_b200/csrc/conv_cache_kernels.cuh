@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(32) conv_varlen_kernel(const ConvArgs<T> a) {
 
 // One token of each sequence: a thread takes VW channels of RB rows, reads each row's K-1 history
 // rows and its new one, and writes the output and the moved history.  The weights are read once
-// for the RB rows.  Bound by latency (slot, then history): 7.0 us for 256 rows of 5376 bf16 channels
-// (22 MB); 26 us with one row and eight channels a thread.
+// for the RB rows.  Bound by latency: the history is asked for only after the walk over the earlier slots.
+// 7.1 us for 256 rows of 5376 bf16 channels (22 MB; 26 us with one row and eight channels a thread), 21
+// for 1024, 116 for 4096, where the walk grows with the square of the rows.
 template <typename T, int K, int VW, int RB>
 __global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs<T> a) {
   const int c0 = int(blockIdx.y * blockDim.x + threadIdx.x) * VW;

@@ -13,11 +13,14 @@
 //   gate first: dy = dv silu(z), dz = dv y silu'(z);  last: dy = dv, dz = dout (n w + b) silu'(z)
 //   dw = sum over rows of do * n,  db = sum over rows of do
 //
-// Everything is read once and kept in registers between the statistics and the result, so HBM
-// bandwidth bounds both; the mean square is taken about the mean (two passes over registers),
-// never as a difference of sums.  At 16384 rows of 5120 channels (float32 y, bf16 z and output) the
-// forward kernel takes 134 us, 5.0 TB/s, and the backward one with its sums 264 us, 4.4 TB/s; both are
-// held back by issue, not by loads (with plain loads and scalar arithmetic: 267 and 642 us).
+// Every value is read once from HBM, whose bandwidth is the floor of both.  The forward kernel keeps a
+// row in registers between its statistics and its result; the backward one reads it from the ring in
+// shared memory again, as its registers are scarce.  The mean square is taken about the mean (a second
+// pass over the values on chip), never as a difference of sums.  At 16384 rows of 5120 channels (float32
+// y, bf16 z and output) the forward kernel takes 135.5 us, 5.0 TB/s, and the backward one with its sums
+// 264 us, 4.4 TB/s; both wait, at 20 warps to an SM, for shared memory and for the sum over the CTA
+// that each row needs (0.45 and 0.56 instructions issued a cycle; with plain loads and scalar
+// arithmetic: 267 and 642 us).
 #pragma once
 #include "conv_cache_kernels.cuh"
 

@@ -85,9 +85,9 @@ __device__ __forceinline__ float softplus_acc(float v) {
 // Why two lanes per channel for 16 states: reading B and C fills registers at 128 bytes a clock
 // and SM, or 256 where a warp reads one or two addresses, and every lane reads its states' B and
 // C anew; with four lanes of four states that takes longer than the exponentials.
-// Measured, 5120 bf16 channels, 16 states, softplus and gate: four prompts of about 4000 tokens in
-// 537 us, 69% of the ex2 rate; ragged ones are bound by the longest, at 79 ns a token.  One prompt of
-// 16384 tokens and 1536 channels, in chunks: 285 us.
+// Measured, 5120 bf16 channels, 16 states, softplus and gate: four prompts of 2300 to 5000 tokens in
+// 528 us, 71% of the ex2 rate; ragged ones are bound by the longest, at 77 ns a token (709 us where it
+// has 9140 of 16384).  One prompt of 16384 tokens and 1536 channels, in chunks: 283.5 us.
 constexpr int kStage = 16;
 
 // The sequence that `rank` others come before, by falling length; nseq <= kSorted.  Call with the
@@ -139,9 +139,10 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
   using RawX = Raw<T, EX, VEC>;
   using RawD = Raw<TD, EX, VEC>;
   using RawB = Raw<T, EB, VEC>;
-  // Wide loads of bf16 rows go through a ring in shared memory, kRing stages deep (ragged prompts at
-  // 5120 channels: 843 -> 724 us, even ones 567 -> 537).  Float32 rows fill twice the ring and the
-  // copies' time: 317 -> 351 us even, 36 -> 42 us for 33 short ones; they go into registers.
+  // Wide loads of bf16 rows go through a ring in shared memory, kRing stages deep (four prompts at
+  // 5120 channels, the longest of 9140 tokens: 840 -> 724 us; of 5020: 565 -> 536).  Float32 rows fill
+  // twice the ring and the copies' time: 317 -> 351 us even, 36 -> 42 us for 33 short ones; they go
+  // into registers.
   constexpr bool RING = VEC && sizeof(T) == 2;
   constexpr int kRing = 2;
   constexpr int kSlot = RING ? 32 * (2 * RawX::kPieces + RawD::kPieces + 2 * RawB::kPieces) : 1;
@@ -545,8 +546,10 @@ __global__ void __launch_bounds__(64, 8) selective_varlen_kernel(const SelArgs a
 // before the first is used.  With four rows each lane of a channel prepares (softplus) and
 // finishes (gate) a row of its own, and hands dt and dt x to the others by shuffles.  VEC: a
 // lane's four states, and its values of B and C, come in one access each.
-// Bound by HBM: 256 rows of 5120 channels, 16 states (184 MB) in 40 us, 4.6 TB/s; 65 us with every
-// lane preparing every row (292 instructions a warp and row).
+// 256 rows of 5120 channels, 16 states (184 MB) in 40 us, 4.6 TB/s; 65 us with every lane preparing
+// every row (292 instructions a warp and row).  Short of HBM's rate because the states are asked for
+// only after the walk over the earlier slots, which grows with the square of the rows (1024 rows: 177
+// us, 4096: 1295).
 template <typename T, typename TD, int LPC, int RB, bool VEC>
 __global__ void __launch_bounds__(128) selective_step_kernel(const SelArgs a) {
   constexpr int OWN = RB == 4 && LPC == 2 ? 2 : 1;  // rows a lane prepares and finishes
